@@ -27,7 +27,10 @@ __all__ = [
     "dwkv_tier_controller_due", "dwkv_tier_controller_threshold", "dwkv_tier_controller_observe",
     "dwkv_tier_controller_route", "dwkv_arena_bytes_all_tiers", "dwkv_basis_sketch", "dwkv_basis_update",
     "dwkv_get_bases", "dwkv_get_moment", "DWKV_ALL_GROUPS", "Cache", "EXPORTED_SYMBOLS",
-    "pack_coeff8", "unpack_coeff8",
+    "pack_coeff8", "unpack_coeff8", "Nibble", "NibbleCache", "dwkv_nibble_config", "nibble_config_from",
+    "dwkv_nibble_config_check", "dwkv_nibble_page_bytes", "dwkv_nibble_pool_bytes", "dwkv_nibble_arena_bytes",
+    "dwkv_nibble_create", "dwkv_nibble_destroy", "dwkv_nibble_tables", "dwkv_nibble_append", "dwkv_nibble_read",
+    "dwkv_nibble_attention", "dwkv_nibble_sync_status",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +51,9 @@ EXPORTED_SYMBOLS = (
     "dwkv_retier", "dwkv_tier_controller_create", "dwkv_tier_controller_destroy", "dwkv_tier_controller_due",
     "dwkv_tier_controller_threshold", "dwkv_tier_controller_observe", "dwkv_tier_controller_route",
     "dwkv_arena_bytes_all_tiers", "dwkv_basis_sketch", "dwkv_basis_update", "dwkv_get_bases", "dwkv_get_moment",
+    "dwkv_nibble_config_check", "dwkv_nibble_page_bytes", "dwkv_nibble_pool_bytes", "dwkv_nibble_arena_bytes",
+    "dwkv_nibble_create", "dwkv_nibble_destroy", "dwkv_nibble_tables", "dwkv_nibble_append", "dwkv_nibble_read",
+    "dwkv_nibble_attention", "dwkv_nibble_sync_status",
 )
 
 
@@ -133,6 +139,7 @@ def lib():
             "dwkv_tier_controller_observe": ([vp, i32, C.c_float, C.POINTER(i32)], C.c_int),
             "dwkv_tier_controller_route": ([vp, i32, i32, vp, vp, i32, vp], C.c_int),
         }
+        sig.update(nibble.signatures())
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -541,3 +548,8 @@ class Cache:
         m = torch.empty(c.num_kv_heads, 2, c.head_dim, c.head_dim, dtype=torch.float32, device=self.device)
         dwkv_get_moment(self.h, group, m, stream)
         return m
+
+
+# ------------------------------------------------------------------------------ the 4-bit cache
+from . import nibble  # noqa: E402  (uses this module's loader and error type)
+from .nibble import *  # noqa: E402,F401,F403

@@ -1,0 +1,331 @@
+// dwkv_nibble_store.cu -- the 4-bit cache's tables (which pages a request holds, where its new
+// rows go), append (quantise rows into their slots) and read (the stored values).
+#include <algorithm>
+
+#include "dwkv_nibble.cuh"
+
+namespace dwkv {
+
+// ------------------------------------------------------------------------------------
+// Tables of a step.  Per slot b: held_b = ceil(len_b / P) pages; a released slot gives its pages
+// back (pushed on the free stack in slot order, then block order) and starts from length 0; then
+// need_b = ceil((len_b + new_b) / P) - ceil(len_b / P) pages come from the top of the stack, in
+// slot order, while the running total of the needs fits.  Row i of slot b gets position
+// len_b + i and slot page * P + position % P; rows of a refused request and rows behind the last
+// one get -1.
+//
+// One cluster does it all.  Every CTA makes the three prefix sums (pages given back, pages
+// needed, rows) in its own shared memory; pushes, pops and rows are then spread flat over the
+// cluster's threads, each finding its request by bisection of a prefix sum, so one long prompt
+// costs no more than many short ones.  The only dependency is pops and in-place updates after
+// pushes and reads: one cluster barrier.
+// ------------------------------------------------------------------------------------
+constexpr int kTabThreads = 1024;
+constexpr int kRowCap = 1 << 30;                 // the prefix sums saturate here
+
+__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kRowCap); }
+
+// Largest i in [0, n) with pre[i] <= x (pre ascending, pre[0] <= x).
+__device__ __forceinline__ int find_in(const int* pre, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+static size_t nib_tables_smem(int n) { return (size_t)(5 * (n + 1) + 3 * 32) * 4; }
+
+__global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G, const NibTables T) {
+    extern __shared__ int tsm[];
+    const int n = T.n, P = G.page;
+    int* back = tsm;                             // [n + 1] exclusive prefix sums
+    int* need = back + n + 1;
+    int* rows = need + n + 1;
+    int* now = rows + n + 1;                     // [n] length before the new rows
+    int* ok = now + n + 1;                       // [n] bit 0 served, bit 1 released
+    int* red = ok + n + 1;                       // [3][32] warp sums
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t rank, ncta;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
+    const long long most = (long long)G.max_blocks * P;
+    const int per = (n + kTabThreads - 1) / kTabThreads;
+    const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
+    int sb = 0, sn = 0, sr = 0;
+    for (int b = b0; b < b1; ++b) {
+        int len = T.len_in[b], nw = T.n_new[b];
+        const bool bad = len < 0 || len > most || nw < 0;
+        const bool rel = !bad && T.release && T.release[b] != 0;
+        int f = rel ? 2 : 0, nd = 0, bk = 0;
+        if (bad) {
+            nw = 0;
+            if (rank == 0) nib_error(G, 10u /*DWKV_DEV_BAD_LENGTH*/, (uint32_t)b, (uint32_t)len);
+        } else {
+            if (rel) { bk = (len + P - 1) / P; len = 0; }
+            if ((long long)len + nw > most) {
+                f |= 4;                          // longer than a table row: refused, its rows still count
+                if (rank == 0) nib_error(G, 10u, (uint32_t)b, (uint32_t)nw);
+            } else {
+                nd = (len + nw + P - 1) / P - (len + P - 1) / P;
+            }
+        }
+        now[b] = len;
+        ok[b] = f;
+        back[b] = bk;
+        need[b] = nd;
+        rows[b] = nw;
+        sb = sat_add(sb, bk);
+        sn = sat_add(sn, nd);
+        sr = sat_add(sr, min(nw, kRowCap));
+    }
+    // block-wide exclusive prefixes of (sb, sn, sr)
+    int pb = sb, pn = sn, pr = sr;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, pb, o), y = __shfl_up_sync(~0u, pn, o), z = __shfl_up_sync(~0u, pr, o);
+        if (lane >= o) { pb = sat_add(pb, x); pn = sat_add(pn, y); pr = sat_add(pr, z); }
+    }
+    if (lane == 31) { red[warp] = pb; red[32 + warp] = pn; red[64 + warp] = pr; }
+    __syncthreads();
+    if (warp == 0) {
+        int x = red[lane], y = red[32 + lane], z = red[64 + lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(~0u, x, o), v = __shfl_up_sync(~0u, y, o), w = __shfl_up_sync(~0u, z, o);
+            if (lane >= o) { x = sat_add(x, u); y = sat_add(y, v); z = sat_add(z, w); }
+        }
+        red[lane] = x; red[32 + lane] = y; red[64 + lane] = z;
+    }
+    __syncthreads();
+    {
+        // exclusive: what the warps and lanes before this thread hold
+        int xb = __shfl_up_sync(~0u, pb, 1), xn = __shfl_up_sync(~0u, pn, 1), xr = __shfl_up_sync(~0u, pr, 1);
+        if (lane == 0) xb = xn = xr = 0;
+        if (warp) { xb = sat_add(xb, red[warp - 1]); xn = sat_add(xn, red[32 + warp - 1]); xr = sat_add(xr, red[64 + warp - 1]); }
+        for (int b = b0; b < b1; ++b) {
+            const int vb = back[b], vn = need[b], vr = rows[b];
+            back[b] = xb; need[b] = xn; rows[b] = xr;
+            xb = sat_add(xb, vb); xn = sat_add(xn, vn); xr = sat_add(xr, min(vr, kRowCap));
+        }
+        if (tid == 0) { back[n] = red[31]; need[n] = red[63]; rows[n] = red[95]; }
+    }
+    __syncthreads();
+    int count = *T.count_in;
+    if (count < 0 || count > G.num_pages) {
+        if (rank == 0 && tid == 0) nib_error(G, 10u, 0xffffffffu, (uint32_t)count);
+        count = max(0, min(count, G.num_pages));
+    }
+    const int all_back = back[n];
+    const int top = min(count + all_back, G.num_pages);
+    if (rank == 0 && tid == 0 && count + all_back > G.num_pages) nib_error(G, 7u /*DWKV_DEV_FREE_LIST*/, (uint32_t)count, (uint32_t)all_back);
+    // served: its pages fit and its rows have a place
+    for (int b = tid; b < n; b += kTabThreads) {
+        const int nd = need[b + 1] - need[b];
+        int f = ok[b];
+        if (!(f & 4)) {
+            if (nd > 0 && need[b + 1] > top) {
+                if (rank == 0) nib_error(G, 1u /*DWKV_DEV_POOL_EXHAUSTED*/, (uint32_t)b, (uint32_t)nd);
+            } else if (rows[b + 1] > T.max_rows) {
+                if (rank == 0) nib_error(G, 13u /*DWKV_DEV_BAD_ROWS*/, (uint32_t)b, (uint32_t)rows[b + 1]);
+            } else {
+                f |= 1;
+            }
+        }
+        ok[b] = f;
+    }
+    const int gt = (int)rank * kTabThreads + tid, gn = (int)ncta * kTabThreads;
+    // push
+    for (int i = gt; i < all_back && count + i < G.num_pages; i += gn) {
+        const int b = find_in(back, n, i);
+        T.free_list[count + i] = T.table[(size_t)b * G.max_blocks + (i - back[b])];
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // pop: page j of the running total is free_list[top - 1 - j]
+    const int all_need = min(need[n], top);
+    for (int i = gt; i < all_need; i += gn) {
+        const int b = find_in(need, n, i);
+        if (ok[b] & 1) T.table[(size_t)b * G.max_blocks + (now[b] + P - 1) / P + (i - need[b])] = T.free_list[top - 1 - i];
+    }
+    // rows
+    for (int r = gt; r < T.max_rows; r += gn) {
+        int pos = -1, slot = -1;
+        if (r < rows[n]) {
+            const int b = find_in(rows, n, r);
+            if (ok[b] & 1) {
+                pos = now[b] + r - rows[b];
+                const int had = (now[b] + P - 1) / P, j = pos / P;
+                const int id = j < had ? T.table[(size_t)b * G.max_blocks + j] : T.free_list[top - 1 - (need[b] + j - had)];
+                slot = id * P + pos % P;
+                if ((unsigned)id >= (unsigned)G.num_pages) {
+                    nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)b, (uint32_t)id);
+                    slot = -1;
+                }
+            }
+        }
+        T.slots[r] = slot;
+        if (T.positions) T.positions[r] = pos;
+    }
+    if (rank == 0) {
+        int taken = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int nw = rows[b + 1] - rows[b];
+            if (ok[b] & 1) taken += need[b + 1] - need[b];
+            // an invalid length is left as it was
+            const int before = T.len_in[b];
+            const bool bad = before < 0 || before > most;
+            T.len_out[b] = bad ? before : now[b] + ((ok[b] & 1) ? nw : 0);
+            T.cu_rows[b] = rows[b];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) taken += __shfl_xor_sync(~0u, taken, o);
+        if (lane == 0) red[warp] = taken;
+        __syncthreads();
+        if (tid == 0) {
+            int s = 0;
+            for (int w = 0; w < kTabThreads / 32; ++w) s += red[w];
+            *T.count_out = top - s;
+            T.cu_rows[n] = rows[n];
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Append: a lane quantises 8 channels of one vector (one 16-byte load), two lanes a block of 16.
+// ------------------------------------------------------------------------------------
+// e5m3 byte of y >= 0 (finite): RNE of y to 4 significant bits (to multiples of 2^-17 below 2^-14).
+__device__ __forceinline__ uint32_t e5m3_of(float y) {
+    y = fminf(y, kNibScaleMax);
+    if (y < 6.103515625e-05f) return (uint32_t)__float2int_rn(y * 131072.f);   // 2^-14; the carry to 8 is 2^-14 itself
+    uint32_t u = __float_as_uint(y);
+    u = (u + 0x7ffffu + ((u >> 20) & 1u)) >> 20;                              // 8 exponent bits, 3 mantissa bits
+    return u - ((127u - 15u) << 3);
+}
+
+template <bool FP16>
+__global__ void __launch_bounds__(256) nib_append_kernel(const NibGeom G, const NibRows R) {
+    const int d = G.d, lv = d >> 3;                                           // lanes of a vector
+    const long long total = (long long)R.n * G.hkv * 2 * lv;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+        const int part = (int)(i % lv);
+        const long long vec = i / lv;
+        const int h = (int)(vec % G.hkv);
+        const long long rz = vec / G.hkv;
+        const int z = (int)(rz & 1);
+        const int row = (int)(rz >> 1);
+        const int slot = R.slots[row];
+        const uint16_t* src = (z ? R.v + row * R.v_stride : R.k + row * R.k_stride) + h * d + part * 8;
+        float x[8];
+        float a = 0.f;
+        bool odd = false;
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = (ws[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+            float f = FP16 ? __half2float(__ushort_as_half((unsigned short)b)) : __uint_as_float(b << 16);
+            odd |= !(fabsf(f) <= 7.f * kNibScaleMax);
+            f = f != f ? 0.f : fminf(fmaxf(f, -7.f * kNibScaleMax), 7.f * kNibScaleMax);
+            x[j] = f;
+            a = fmaxf(a, fabsf(f));
+        }
+        // the two lanes of a block are neighbours (total is a multiple of 8)
+        a = fmaxf(a, __shfl_xor_sync(3u << (threadIdx.x & 30u), a, 1));
+        const uint32_t sb = e5m3_of(__fdiv_rn(a, 7.f));
+        const float s = nib_scale((uint8_t)sb);
+        uint32_t u = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = sb ? max(-7, min(7, __float2int_rn(__fdiv_rn(x[j], s)))) : 0;
+            u |= (uint32_t)(c + 8) << (4 * j);
+        }
+        // each 16-bit unit rotated left by 2
+        u = ((u << 2) & 0xfffcfffcu) | ((u >> 14) & 0x00030003u);
+        if (slot == -1) continue;
+        if ((unsigned)slot >= (unsigned)G.num_pages * (unsigned)G.page) {
+            nib_error(G, 12u /*DWKV_DEV_BAD_SLOT*/, (uint32_t)row, (uint32_t)slot);
+            continue;
+        }
+        if (odd) nib_error(G, 9u /*DWKV_DEV_RANGE*/, (uint32_t)row, (uint32_t)(2 * h + z));
+        const int tok = slot % G.page, t = tok & 15;
+        uint8_t* blk = R.pool + nib_block_at(G, slot / G.page, h, tok);
+        *reinterpret_cast<uint32_t*>(blk + (z ? nib_v_off(d, t, 4 * part) : nib_k_off(d, t) + 4 * part)) = u;
+        if (!(part & 1)) blk[z ? nib_vscale_off(d, t, part >> 1) : nib_kscale_off(d, t, part >> 1)] = (uint8_t)sb;
+    }
+}
+
+// The stored values of the given slots (zeros for -1), in the caller's 16-bit type: exact.
+template <bool FP16>
+__global__ void __launch_bounds__(256) nib_read_kernel(const NibGeom G, const NibRows R) {
+    const int d = G.d, lv = d >> 3;
+    const long long total = (long long)R.n * G.hkv * 2 * lv;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+        const int part = (int)(i % lv);
+        const long long vec = i / lv;
+        const int h = (int)(vec % G.hkv);
+        const long long rz = vec / G.hkv;
+        const int z = (int)(rz & 1);
+        const int row = (int)(rz >> 1);
+        const int slot = R.slots[row];
+        uint32_t o[4] = {0, 0, 0, 0};
+        if (slot != -1) {
+            if ((unsigned)slot >= (unsigned)G.num_pages * (unsigned)G.page) {
+                nib_error(G, 12u, (uint32_t)row, (uint32_t)slot);
+            } else {
+                const int tok = slot % G.page, t = tok & 15;
+                const uint8_t* blk = R.pool + nib_block_at(G, slot / G.page, h, tok);
+                uint32_t u = *reinterpret_cast<const uint32_t*>(blk + (z ? nib_v_off(d, t, 4 * part) : nib_k_off(d, t) + 4 * part));
+                const float s = nib_scale(blk[z ? nib_vscale_off(d, t, part >> 1) : nib_kscale_off(d, t, part >> 1)]);
+                u = ((u >> 2) & 0x3fff3fffu) | ((u & 0x00030003u) << 14);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float f = (float)((int)((u >> (4 * j)) & 15u) - 8) * s;
+                    const uint32_t b = FP16 ? (uint32_t)__half_as_ushort(__float2half_rn(f)) : __float_as_uint(f) >> 16;
+                    o[j >> 1] |= b << (16 * (j & 1));
+                }
+            }
+        }
+        uint16_t* dst = (z ? R.v_out : R.k_out) + ((size_t)row * G.hkv + h) * d + part * 8;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+cudaError_t nib_prepare_store() {
+    return cudaFuncSetAttribute(nib_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)nib_tables_smem(kNibMaxSeqs));
+}
+
+cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s) {
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = (T.n > 1024 || T.max_rows > 2048) ? 8 : 1;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    c.gridDim = dim3(a.val.clusterDim.x);
+    c.blockDim = dim3(kTabThreads);
+    c.dynamicSmemBytes = nib_tables_smem(T.n);
+    c.stream = s;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, nib_tables_kernel, G, T);
+}
+
+static unsigned row_grid(const NibGeom& G, const NibRows& R, int sms) {
+    const long long lanes = (long long)R.n * G.hkv * 2 * (G.d >> 3);
+    return (unsigned)std::max(1ll, std::min((lanes + 255) / 256, 8ll * sms));
+}
+
+cudaError_t nib_append(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s) {
+    if (G.fp16) nib_append_kernel<true><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
+    else nib_append_kernel<false><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
+    return cudaGetLastError();
+}
+
+cudaError_t nib_read(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s) {
+    if (G.fp16) nib_read_kernel<true><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
+    else nib_read_kernel<false><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
+    return cudaGetLastError();
+}
+
+}  // namespace dwkv

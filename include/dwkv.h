@@ -79,6 +79,11 @@ typedef enum {
 #define DWKV_DEV_TIMEOUT 6          /* a bounded wait in a kernel ran out                 */
 #define DWKV_DEV_FREE_LIST 7        /* free-page ring overflow on reset                   */
 #define DWKV_DEV_BASIS 8            /* basis construction: a sketch column vanished        */
+#define DWKV_DEV_RANGE 9            /* 4-bit append: a value NaN, infinite or beyond 53760 */
+#define DWKV_DEV_BAD_LENGTH 10      /* 4-bit cache: a length or count out of range         */
+#define DWKV_DEV_BAD_PAGE 11        /* 4-bit cache: a page id outside the pool             */
+#define DWKV_DEV_BAD_SLOT 12        /* 4-bit cache: a slot outside the pool                */
+#define DWKV_DEV_BAD_ROWS 13        /* 4-bit cache: a request's rows do not fit the call   */
 
 /* Cache geometry.  Supported by this build: head_dim == 128; num_q_heads == 4 *
  * num_kv_heads; tiers drawn from {8, 16, 32, 64, 128}, strictly ascending, each <= r_max;
@@ -450,6 +455,122 @@ size_t dwkv_quantize_work_bytes(int32_t n, int32_t s, int32_t bits);
 dwkv_status dwkv_quantize_residuals(int32_t n, int32_t s, int32_t bits, const float* r, uint8_t* idx,
                                     int8_t* codes, uint16_t* scales, void* work, size_t work_bytes,
                                     void* stream);
+
+/* ---- The 4-bit cache: every channel kept.  Next to the factored cache above, for layers or
+ * requests whose keys and values a low-rank basis does not fit: each vector of head_dim channels
+ * is stored whole, in 4 bits a channel with an 8-bit scale per 16 channels (4.5 bits a value).
+ *
+ * Codec, per 16 channels x of a vector: s = max |x| / 7 rounded to nearest even to 4 significant
+ * bits (multiples of 2^-17 below 2^-14; at most 7680), code = clamp(rint(x / s), -7, 7), 0 where
+ * s = 0; the stored value is code * s, exact in bf16 and fp16.  The scale byte is an unsigned
+ * e5m3 number: s is the fp16 number of bits (byte << 7).  A NaN is stored as 0 and magnitudes
+ * above 53760 as 53760; both record DWKV_DEV_RANGE.
+ *
+ * The pool is num_pages pages of page_tokens tokens, each page [kv-head][page_tokens / 16] blocks
+ * of 16 tokens, 18 head_dim bytes a block:
+ *   key units    [16][head_dim/4] uint16, unit = four consecutive channels:
+ *                sum of (code_j + 8) << 4 j, rotated left by 2 bits
+ *   key scales   [16][head_dim/16] bytes
+ *   value units  as the keys', the 16-byte chunk c of token t at chunk c ^ ((t >> 1) & 3)
+ *                (head_dim 128) or c ^ ((t >> 2) & 1) (head_dim 64)
+ *   value scales group g of token t at ((4 (g & 1) + (t & 7) / 2) (head_dim / 32) + g / 2) 4 +
+ *                (t & 1) + 2 (t / 8)
+ * A token's slot is page * page_tokens + position % page_tokens.  A layer has a pool of its own;
+ * the tables below serve every layer of a model.
+ *
+ * The caller owns everything: pools, tables and the handle's arena (device, 256-byte aligned,
+ * dwkv_nibble_arena_bytes).  The handle keeps the configuration and, in the arena, the device
+ * error word and the attention's workspace: calls on one handle go to one stream at a time, and
+ * graphs captured from one handle are replayed one after the other, not side by side.  Calls run
+ * on the handle's device whatever the current one is.  No call reads device data on the host, so
+ * all of them but create and sync_status may be captured; lengths, counts and tables then
+ * advance on the GPU at each replay. */
+#define DWKV_BF16 0
+#define DWKV_FP16 1
+typedef struct {
+    int32_t num_q_heads;       /* a multiple of num_kv_heads, up to 64 times as many        */
+    int32_t num_kv_heads;
+    int32_t head_dim;          /* 64 or 128                                                 */
+    int32_t page_tokens;       /* 16, 32, 64 or 128                                         */
+    int32_t num_pages;         /* pages of a pool (num_pages * page_tokens < 2^31)          */
+    int32_t max_seqs;          /* request slots, at most 8192                               */
+    int32_t max_blocks;        /* pages of a request: the row length of block_tables        */
+    int32_t dtype;             /* of k, v, q and out: DWKV_BF16 or DWKV_FP16                */
+    int32_t window;            /* 0, or: a row sees the last `window` positions only        */
+    float softmax_scale;       /* <= 0 selects 1/sqrt(head_dim)                             */
+} dwkv_nibble_config;
+typedef struct dwkv_nibble_ctx* dwkv_nibble_handle;
+
+/* Validates a configuration without touching the GPU; bytes of a page, a pool and the arena
+ * (0 if the configuration is invalid). */
+dwkv_status dwkv_nibble_config_check(const dwkv_nibble_config* cfg);
+size_t dwkv_nibble_page_bytes(const dwkv_nibble_config* cfg);
+size_t dwkv_nibble_pool_bytes(const dwkv_nibble_config* cfg);
+size_t dwkv_nibble_arena_bytes(const dwkv_nibble_config* cfg);
+
+/* A handle on the current device; its arena is cleared on `stream`.  destroy waits for nothing. */
+dwkv_status dwkv_nibble_create(const dwkv_nibble_config* cfg, void* arena, size_t arena_bytes, void* stream,
+                               dwkv_nibble_handle* out);
+dwkv_status dwkv_nibble_destroy(dwkv_nibble_handle h);
+
+/* One step's block tables and slot map from the requests' lengths, on the GPU.  For request slot
+ * b in [0, n_seqs), P = page_tokens:
+ *   release[b] != 0 (release may be NULL): the slot's ceil(seq_lens[b] / P) pages go back on the
+ *     free stack (free_list[0 .. *free_count), the top last), in slot order and table order, and
+ *     its length becomes 0;
+ *   then n_new[b] >= 0 rows are added: ceil((len + n_new) / P) - ceil(len / P) pages are taken
+ *     from the top of the stack, in slot order, and written behind the slot's pages in
+ *     block_tables [n_seqs][max_blocks].
+ * Outputs: seq_lens_out [n_seqs]; free_count_out [1]; cu_rows [n_seqs + 1], the running total of
+ * n_new; positions (may be NULL) and slots [max_rows]: row cu_rows[b] + i has position len + i
+ * and the slot that the tables give it; rows behind the last get -1 in both.  seq_lens_out may be
+ * seq_lens and free_count_out may be free_count; apart from them no array overlaps another.
+ * free_list has num_pages entries.
+ * A request is refused whole, its length and pages as they were and its rows -1, when the
+ * running total of the pages needed (its own and the slots' before it) exceeds the free pages
+ * (DWKV_DEV_POOL_EXHAUSTED), when it would outgrow max_blocks (DWKV_DEV_BAD_LENGTH) or when its
+ * rows end behind max_rows (DWKV_DEV_BAD_ROWS).  A length or count out of range leaves its slot
+ * as it is, with no rows (DWKV_DEV_BAD_LENGTH). */
+dwkv_status dwkv_nibble_tables(dwkv_nibble_handle h, int32_t n_seqs, const int32_t* n_new, const int32_t* release,
+                               const int32_t* seq_lens, int32_t* block_tables, int32_t* free_list,
+                               const int32_t* free_count, int32_t* seq_lens_out, int32_t* free_count_out,
+                               int32_t max_rows, int32_t* cu_rows, int32_t* positions, int32_t* slots, void* stream);
+
+/* Quantises n_rows rows of keys and values into their slots of one layer's pool.
+ *   k, v  : device, [n_rows][num_kv_heads][head_dim] of the configured type, k_stride / v_stride
+ *           elements between rows (multiples of 8; views of a fused projection are fine),
+ *           16-byte aligned
+ *   slots : device int32 [n_rows]; -1 skips the row; other slots outside the pool are skipped
+ *           and record DWKV_DEV_BAD_SLOT.  Slots of one call are distinct. */
+dwkv_status dwkv_nibble_append(dwkv_nibble_handle h, int32_t n_rows, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int32_t* slots, void* pool, void* stream);
+
+/* The stored values of n_rows slots, exact, in the configured type: k_out and v_out device
+ * [n_rows][num_kv_heads][head_dim], 16-byte aligned.  Slot -1 gives zeros. */
+dwkv_status dwkv_nibble_read(dwkv_nibble_handle h, int32_t n_rows, const int32_t* slots, const void* pool, void* k_out,
+                             void* v_out, void* stream);
+
+/* Causal attention of each request's newest rows over its cached tokens.  Request b has the rows
+ * cu_rows[b] .. cu_rows[b + 1) of q (n of them, n <= max_q) and seq_lens[b] cached tokens, its new
+ * ones included: row j stands at position p = seq_lens[b] - n + j and sees the tokens t with
+ * max(0, p - window + 1) <= t <= p (from 0 without a window).
+ *   o = sum_t softmax_t(softmax_scale q . k_t) v_t ; lse = log sum_t exp(softmax_scale q . k_t)
+ * A row that sees nothing (p < 0) gives o = 0 and lse = -inf.
+ *   q   : device [n_rows][num_q_heads][head_dim], q_stride elements between rows (a multiple of
+ *         8), 16-byte aligned
+ *   out : device [n_rows][num_q_heads][head_dim]; lse: NULL or device fp32 [n_rows][num_q_heads].
+ *         Rows that no request has are left as they were.
+ *   max_q : the most rows of one request.  It chooses the kernel and bounds the launch; a request
+ *         with more is skipped (DWKV_DEV_BAD_ROWS), as is one whose length is out of range
+ *         (DWKV_DEV_BAD_LENGTH).  Tokens in a page outside the pool are left out
+ *         (DWKV_DEV_BAD_PAGE).
+ * What lies in the pool behind a request's last token is not looked at, NaN patterns included. */
+dwkv_status dwkv_nibble_attention(dwkv_nibble_handle h, int32_t n_seqs, int32_t n_rows, int32_t max_q, const void* q,
+                                  int64_t q_stride, const int32_t* cu_rows, const int32_t* seq_lens,
+                                  const int32_t* block_tables, const void* pool, void* out, float* lse, void* stream);
+
+/* As dwkv_sync_status, for the handle's error word. */
+dwkv_status dwkv_nibble_sync_status(dwkv_nibble_handle h, void* stream);
 
 #ifdef __cplusplus
 }

@@ -93,13 +93,19 @@ struct NibAttend {
     const uint8_t* pool;
     uint16_t* out;                               // [n_rows][hq][d]
     float* lse;                                  // nullable [n_rows][hq]
+    int rows_hi;                                 // requests with more rows x heads than this are not this launch's
+    int* tickets;                                // [CTAs] zero between launches
+    float* records;                              // [2 CTAs] parts of requests cut between CTAs
 };
 
 cudaError_t nib_prepare_store();
 cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s);
 cudaError_t nib_append(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s);
 cudaError_t nib_read(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s);
-cudaError_t nib_attend(const NibGeom& G, const NibAttend& A, int sms, cudaStream_t s);
+// Bytes of the handle's arena behind its first 256 (the error word): tickets, records.
+size_t nib_attend_bytes(int d);
+cudaError_t nib_prepare_attend(const NibGeom& G);
+cudaError_t nib_attend(const NibGeom& G, NibAttend A, int sms, uint8_t* arena, cudaStream_t s);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void nib_error(const NibGeom& G, uint32_t code, uint32_t a, uint32_t b) {
@@ -125,6 +131,28 @@ __device__ __forceinline__ bool nib_request(const NibGeom& G, const NibAttend& A
     }
     nq = c1 - c0;
     return true;
+}
+
+// Four channels of row r (of a kv-head's rows x heads) of a request whose rows start at row0: the
+// output (o in units of 1/32, unnormalised against the maximum mm - 7 in log2 units and the sum ll).
+template <bool FP16>
+__device__ __forceinline__ void nib_put(const NibGeom& G, const NibAttend& A, int row0, int h, int r, int d, int ch, float mm,
+                                        float ll, float4 o) {
+    const int j = r / G.g;
+    const size_t at = (size_t)(row0 + j) * G.hq + (size_t)(h * G.g + r - j * G.g);
+    const float inv = ll > 0.f ? 32.f / ll : 0.f;
+    uint32_t lo, hi;
+    if (FP16) {
+        const __half2 a = __floats2half2_rn(o.x * inv, o.y * inv), b = __floats2half2_rn(o.z * inv, o.w * inv);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint2*>(A.out + at * d + ch) = make_uint2(lo, hi);
+    if (A.lse && ch == 0) A.lse[at] = ll > 0.f ? (mm - 7.f + log2f(ll)) * 0.6931471805599453f : -INFINITY;
 }
 
 __device__ __forceinline__ float nib_scale(uint8_t b) { return __half2float(__ushort_as_half((unsigned short)(b << 7))); }

@@ -127,7 +127,8 @@ dwkv_status check_rows(const NibGeom& G, int32_t n, const void* k, int64_t ks, c
     return DWKV_OK;
 }
 
-size_t arena_need() { return 256; }
+// The error word, then the attention's tickets and records.
+size_t arena_need(const dwkv_nibble_config* c) { return 256 + nib_attend_bytes(c->head_dim); }
 
 }  // namespace
 
@@ -147,7 +148,7 @@ size_t dwkv_nibble_pool_bytes(const dwkv_nibble_config* cfg) {
 
 size_t dwkv_nibble_arena_bytes(const dwkv_nibble_config* cfg) {
     if (check_cfg(cfg) != DWKV_OK) return 0;
-    return arena_need();
+    return arena_need(cfg);
 }
 
 dwkv_status dwkv_nibble_create(const dwkv_nibble_config* cfg, void* arena, size_t arena_bytes, void* stream,
@@ -157,8 +158,8 @@ dwkv_status dwkv_nibble_create(const dwkv_nibble_config* cfg, void* arena, size_
     *out = nullptr;
     if ((st = check_cfg(cfg)) != DWKV_OK) return st;
     if (!arena || misaligned(arena, 256)) return fail(DWKV_ERR_INVALID_ARG, "arena must be non-NULL and 256-byte aligned");
-    if (arena_bytes < arena_need())
-        return fail(DWKV_ERR_CAPACITY, "arena of %zu bytes is below the %zu needed", arena_bytes, arena_need());
+    if (arena_bytes < arena_need(cfg))
+        return fail(DWKV_ERR_CAPACITY, "arena of %zu bytes is below the %zu needed", arena_bytes, arena_need(cfg));
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -169,7 +170,8 @@ dwkv_status dwkv_nibble_create(const dwkv_nibble_config* cfg, void* arena, size_
         return fail(DWKV_ERR_INVALID_ARG, "arena must be device memory of the current device %d", dev);
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = nib_prepare_store();
-    if (e == cudaSuccess) e = cudaMemsetAsync(arena, 0, arena_need(), static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = nib_prepare_attend(make_geom(cfg));
+    if (e == cudaSuccess) e = cudaMemsetAsync(arena, 0, arena_need(cfg), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "dwkv_nibble_create");
     auto* h = new (std::nothrow) dwkv_nibble_ctx();
     if (!h) return fail(DWKV_ERR_CAPACITY, "out of host memory");
@@ -262,8 +264,8 @@ dwkv_status dwkv_nibble_attention(dwkv_nibble_handle h, int32_t n_seqs, int32_t 
     if ((st = check_pool(pool)) != DWKV_OK) return st;
     NIB_DEVICE(h);
     const NibAttend A{n_seqs, n_rows, std::min(max_q, n_rows), q_stride, static_cast<const uint16_t*>(q), cu_rows, seq_lens,
-                      block_tables, static_cast<const uint8_t*>(pool), static_cast<uint16_t*>(out), lse};
-    const cudaError_t e = nib_attend(G, A, h->num_sms, static_cast<cudaStream_t>(stream));
+                      block_tables, static_cast<const uint8_t*>(pool), static_cast<uint16_t*>(out), lse, 0, nullptr, nullptr};
+    const cudaError_t e = nib_attend(G, A, h->num_sms, h->arena, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "dwkv_nibble_attention launch");
     return DWKV_OK;
 }

@@ -1,5 +1,7 @@
 // dwkv_nibble_attend.cu -- attention over the 4-bit cache.
-#include "dwkv_nibble.cuh"
+#include <algorithm>
+
+#include "dwkv_nibble_decode.cuh"
 
 namespace dwkv {
 
@@ -18,7 +20,7 @@ __global__ void __launch_bounds__(128) nib_attend_simple_kernel(const NibGeom G,
     }
     if (lo >= A.n) return;                                    // behind the last row
     int len, nq;
-    if (!nib_request(G, A, lo, len, nq)) return;
+    if (!nib_request(G, A, lo, len, nq) || nq * G.g <= A.rows_hi) return;
     const int pos = len - nq + (row - A.cu[lo]);
     const int first = G.window > 0 ? max(0, pos - G.window + 1) : 0;
     float q[C], o[C];
@@ -72,7 +74,52 @@ __global__ void __launch_bounds__(128) nib_attend_simple_kernel(const NibGeom G,
     if (A.lse && lane == 0) A.lse[(size_t)row * G.hq + head] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
-cudaError_t nib_attend(const NibGeom& G, const NibAttend& A, int sms, cudaStream_t s) {
+// ------------------------------------------------------------------------------ launches
+constexpr int kNdRows = 16;                                   // rows x heads that the decode kernels take
+constexpr int kMaxSms = 160;
+
+static constexpr size_t kTicketBytes = (size_t)2 * kMaxSms * 4;
+
+size_t nib_attend_bytes(int d) { return kTicketBytes + (size_t)2 * kMaxSms * 16 * (d + 2) * 4; }
+
+template <int D, int NT, bool SPLIT, bool FP16>
+static cudaError_t decode_launch(const NibGeom& G, const NibAttend& A, int sms, cudaStream_t s, bool prepare) {
+    using L = NdLayout<D, NT>;
+    auto k = nib_decode_kernel<D, NT, SPLIT, FP16>;
+    if (prepare) return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
+    k<<<std::min(sms, kMaxSms) * L::kCtas, kNdThreads, L::kBytes, s>>>(G, A);
+    return cudaGetLastError();
+}
+
+// The instantiation for up to `rows` rows x heads a request.
+static cudaError_t decode_rows(const NibGeom& G, const NibAttend& A, int rows, int sms, cudaStream_t s, bool prepare) {
+#define NIB_PICK(D, F)                                                                          \
+    return rows <= 4 ? decode_launch<D, 1, true, F>(G, A, sms, s, prepare)                      \
+         : rows <= 8 ? decode_launch<D, 1, false, F>(G, A, sms, s, prepare)                     \
+                     : decode_launch<D, 2, false, F>(G, A, sms, s, prepare)
+    if (G.d == 128) {
+        if (G.fp16) NIB_PICK(128, true);
+        NIB_PICK(128, false);
+    }
+    if (G.fp16) NIB_PICK(64, true);
+    NIB_PICK(64, false);
+#undef NIB_PICK
+}
+
+cudaError_t nib_prepare_attend(const NibGeom& G) {
+    cudaError_t e = cudaSuccess;
+    for (int rows : {4, 8, 16})
+        if (e == cudaSuccess) e = decode_rows(G, NibAttend{}, rows, 0, nullptr, true);
+    return e;
+}
+
+cudaError_t nib_attend(const NibGeom& G, NibAttend A, int sms, uint8_t* arena, cudaStream_t s) {
+    A.tickets = reinterpret_cast<int*>(arena + 256);
+    A.records = reinterpret_cast<float*>(arena + 256 + kTicketBytes);
+    const long long most = (long long)A.max_q * G.g;          // rows x heads of a request at most
+    A.rows_hi = (int)std::min<long long>(most, kNdRows);
+    cudaError_t e = decode_rows(G, A, A.rows_hi, sms, s, false);
+    if (e != cudaSuccess || most <= kNdRows) return e;
     const unsigned grid = (unsigned)(((long long)A.n_rows * G.hq + 3) / 4);
     if (G.d == 128) {
         if (G.fp16) nib_attend_simple_kernel<128, true><<<grid, 128, 0, s>>>(G, A);

@@ -26,7 +26,7 @@ constexpr int kNibMaxSeqs = 8192;                // sequence slots (the table ke
 constexpr float kNibScaleMax = 7680.f;           // largest scale; 7 * 7680 = 53760 the largest value
 
 struct NibGeom {
-    int hq, hkv, g, d, page, per, num_pages, max_seqs, max_blocks, window, fp16;
+    int hq, hkv, g, d, page, page_shift, per, num_pages, max_seqs, max_blocks, window, fp16;
     float tau;
     uint32_t blk;                                // bytes of a block
     size_t page_bytes;

@@ -71,6 +71,7 @@ NibGeom make_geom(const dwkv_nibble_config* c) {
     G.g = c->num_q_heads / c->num_kv_heads;
     G.d = c->head_dim;
     G.page = c->page_tokens;
+    while ((1 << G.page_shift) < c->page_tokens) ++G.page_shift;
     G.per = c->page_tokens / kNibBlock;
     G.num_pages = c->num_pages;
     G.max_seqs = c->max_seqs;

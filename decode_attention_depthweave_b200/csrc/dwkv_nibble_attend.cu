@@ -82,21 +82,21 @@ static constexpr size_t kTicketBytes = (size_t)2 * kMaxSms * 4;
 
 size_t nib_attend_bytes(int d) { return kTicketBytes + (size_t)2 * kMaxSms * 16 * (d + 2) * 4; }
 
-template <int D, int NT, bool SPLIT, bool FP16>
+template <int D, int R, bool FP16>
 static cudaError_t decode_launch(const NibGeom& G, const NibAttend& A, int sms, cudaStream_t s, bool prepare) {
-    using L = NdLayout<D, NT>;
-    auto k = nib_decode_kernel<D, NT, SPLIT, FP16>;
+    using L = NdLayout<D, R>;
+    auto k = nib_decode_kernel<D, R, R == 4 && FP16, FP16>;
     if (prepare) return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
-    k<<<std::min(sms, kMaxSms) * L::kCtas, kNdThreads, L::kBytes, s>>>(G, A);
+    k<<<std::min(sms, kMaxSms) * L::kCtas, kNdThreads + 32, L::kBytes, s>>>(G, A);
     return cudaGetLastError();
 }
 
 // The instantiation for up to `rows` rows x heads a request.
 static cudaError_t decode_rows(const NibGeom& G, const NibAttend& A, int rows, int sms, cudaStream_t s, bool prepare) {
 #define NIB_PICK(D, F)                                                                          \
-    return rows <= 4 ? decode_launch<D, 1, true, F>(G, A, sms, s, prepare)                      \
-         : rows <= 8 ? decode_launch<D, 1, false, F>(G, A, sms, s, prepare)                     \
-                     : decode_launch<D, 2, false, F>(G, A, sms, s, prepare)
+    return rows <= 4 ? decode_launch<D, 4, F>(G, A, sms, s, prepare)                      \
+         : rows <= 8 ? decode_launch<D, 8, F>(G, A, sms, s, prepare)                     \
+                     : decode_launch<D, 16, F>(G, A, sms, s, prepare)
     if (G.d == 128) {
         if (G.fp16) NIB_PICK(128, true);
         NIB_PICK(128, false);

@@ -9,15 +9,17 @@
 //    contiguous ranges, one a CTA: any mix of lengths loads the SMs evenly, and no host code
 //    has to know a length.  A (request, kv-head) cut by a range end leaves records that the last
 //    CTA to finish merges (an atomic ticket, no wait).
-//  - A warp takes the 16-token blocks w, w + kWarps, ... of a range.  It keeps its own ring of
-//    blocks in flight (bulk copies on mbarriers, across request borders), its own maximum, sum and
-//    accumulator: warps meet only where a (request, kv-head) ends.
+//  - A consumer warp takes two 16-token blocks of each unit and keeps its own maximum, sum and
+//    accumulator: consumers meet only where a (request, kv-head) ends.  A producer warp keeps a ring
+//    of blocks in flight for each of them (bulk copies on mbarriers, across request borders), a
+//    lane a block, and refills a warp's stage when that warp has read it: with stages shared by all
+//    warps, the slowest held up the copies of the others (75 -> 109 us at two stages of 36 KB).
 //  - S^T = K Q^T: tokens are the 16 MMA rows, query rows the 8 columns; a lane reads 16 bytes of
 //    two tokens' codes and unpacks them to fp16 (exact) in registers.  O^T = V^T P^T: channels are
 //    the MMA rows, ldmatrix.trans pairs two tokens' units, P is transposed by movmatrix.
-//  - Up to 4 rows, the columns 4-7 hold the same queries again, and P's rounding remainder in the
-//    value product: P is then good to 22 bits at no cost.  Beyond, P is fp16 (11 bits), like the
-//    output's own rounding or finer.
+//  - P is rounded to fp16 (11 bits) for the value product: finer than a bf16 output.  An fp16
+//    output of up to 4 rows gets P's remainder too: the columns 4-7 hold the same queries again,
+//    and in the value product what the rounding left, so P is good to 22 bits.
 //  - P carries 2^7: with the maximum allowed to lag 2^8 behind, it stays below 2^15, and weights
 //    down to 2^-31 keep a bit.
 #pragma once
@@ -25,23 +27,30 @@
 
 namespace dwkv {
 
-constexpr int kNdWarps = 8;
-constexpr int kNdThreads = 32 * kNdWarps;
-constexpr int kNdUnit = kNibBlock * kNdWarps;            // tokens of a unit
+// Seven consumers and the producer are 8 warps: two CTAs an SM leave a thread 128 registers, and the
+// loop's accumulators, scores and fragments fit (with eight consumers, 96: it spilled, 75 -> 110 us).
+constexpr int kNdWarps = 7;
+constexpr int kNdThreads = 32 * kNdWarps;               // consumers; one more warp produces
+constexpr int kNdSub = 2;                                // blocks that a warp takes at a time
+constexpr int kNdBlocks = kNdSub * kNdWarps;             // blocks of a unit
+constexpr int kNdUnit = kNibBlock * kNdBlocks;           // tokens of a unit
 constexpr float kNdNone = -1e30f;                        // maximum of nothing
 constexpr float kNdLag = 8.f, kNdBias = 7.f;             // log2
 
-template <int D, int NT>
+template <int D, int R>
 struct NdLayout {
-    static constexpr int kStages = D == 128 ? (NT == 1 ? 4 : 6) : (NT == 1 ? 8 : 12);
-    static constexpr int kCtas = NT == 1 ? 2 : 1;        // an SM
+    static constexpr int kMr = R < 8 ? R : 8;            // rows merged at a time
+    static constexpr int kCtas = R <= 8 ? 2 : 1;         // an SM
+    static constexpr int kStages = (D == 128 ? 1 : 2) * (R <= 4 ? 3 : R <= 8 ? 2 : 4);
     static constexpr uint32_t kBlock = 18u * D;
+    static constexpr uint32_t kStage = kNdSub * kBlock;  // of one warp
     static constexpr int kPitch = D + 4;                 // floats of a merge row: 16-byte accesses of a warp fall in distinct banks
-    static constexpr uint32_t kRing = (uint32_t)kNdWarps * kStages * kBlock;
-    static constexpr uint32_t kMerge = kRing;                                    // [warps][8][kPitch] fp32
-    static constexpr uint32_t kMl = kMerge + (uint32_t)kNdWarps * 8 * kPitch * 4;   // m [warps][8 NT], l [warps][8 NT]
-    static constexpr uint32_t kBars = kMl + (uint32_t)kNdWarps * 8 * NT * 8;
-    static constexpr uint32_t kScan = kBars + (uint32_t)kNdWarps * kStages * 8;     // scan scratch, 128 bytes
+    static constexpr uint32_t kMerge = (uint32_t)kNdWarps * kStages * kStage;       // [warps][kMr][kPitch] fp32
+    static constexpr uint32_t kMl = kMerge + (uint32_t)kNdWarps * kMr * kPitch * 4; // m [warps][16], l [warps][16]
+    static constexpr uint32_t kQ = kMl + (uint32_t)kNdWarps * 16 * 8;               // the queries' fragments [tiles][D/32][lane] 16 bytes
+    static constexpr uint32_t kBars = kQ + (R > 8 ? 2u : 1u) * (D / 32) * 512;      // full [warps][stages], empty [warps][stages]
+    static constexpr uint32_t kFlags = kBars + 2u * kNdWarps * kStages * 8;         // [warps][stages][2] bytes: bit 0 not there, bit 1 seen in part
+    static constexpr uint32_t kScan = (kFlags + 2u * kNdWarps * kStages + 15u) & ~15u;         // scan scratch, 128 bytes
     static constexpr uint32_t kBytes = kScan + 128;
 };
 
@@ -64,14 +73,40 @@ __device__ __forceinline__ uint32_t hmul2_(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ void nib_unpack(uint32_t u, uint32_t r, uint32_t b0, uint32_t b1, uint32_t (&o)[4]) {
+// e8, eh: 8 and 1/2 as fp16 pairs, in registers (a LOP3 takes one immediate; of two, the compiler
+// makes two instructions).
+__device__ __forceinline__ uint32_t reg_const(uint32_t v) {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void nib_unpack(uint32_t u, uint32_t r, uint32_t b0, uint32_t b1, uint32_t e8, uint32_t eh, uint32_t (&o)[4]) {
     const uint32_t w = __byte_perm(u, 0, 0x2301);
-    o[0] = hfma2_(lop_and_or(u, 0x003c003cu, 0x48004800u), r, b0);
-    o[1] = hfma2_(lop_and_or(u, 0x03c003c0u, 0x38003800u), r, b1);
-    o[2] = hfma2_(lop_and_or(w, 0x003c003cu, 0x48004800u), r, b0);
-    o[3] = hfma2_(lop_and_or(w, 0x03c003c0u, 0x38003800u), r, b1);
+    o[0] = hfma2_(lop_and_or(u, 0x003c003cu, e8), r, b0);
+    o[1] = hfma2_(lop_and_or(u, 0x03c003c0u, eh), r, b1);
+    o[2] = hfma2_(lop_and_or(w, 0x003c003cu, e8), r, b0);
+    o[3] = hfma2_(lop_and_or(w, 0x03c003c0u, eh), r, b1);
+}
+// D (16x8 f32) = A (16x16 f16, row) * B (16x8 f16, col)
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 constexpr uint32_t kNibB0 = 0xc820c820u, kNibB1 = 0xba00ba00u;      // -8.25, -0.75 as fp16 pairs
+// One poll of an mbarrier's phase that may sleep for a fraction of a microsecond.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(200u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ uint32_t movm_t(uint32_t a) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -142,138 +177,183 @@ struct NdWalk {
     }
 };
 
-// One record of a cut (request, kv-head): [rows] m, [rows] l, [rows][D] unnormalised o.
-template <int D>
-__host__ __device__ constexpr int nd_record_floats(int rows) { return rows * (D + 2); }
+// A record of a cut (request, kv-head): [R] m, [R] l, [R][D] unnormalised o.
 
-template <int D, int NT, bool SPLIT, bool FP16>
-__global__ void __launch_bounds__(kNdThreads, NdLayout<D, NT>::kCtas) nib_decode_kernel(const NibGeom G, const NibAttend A) {
-    using L = NdLayout<D, NT>;
-    constexpr int R = SPLIT ? 4 : 8 * NT;                // rows of a request at most
-    constexpr int kKs = D / 16, kWords = D / 32, kChunks = D / 32;
+template <int D, int R, bool SPLIT, bool FP16>
+__global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_decode_kernel(const NibGeom G, const NibAttend A) {
+    using L = NdLayout<D, R>;
+    constexpr int NT = R > 8 ? 2 : 1;                    // MMA column tiles
+    constexpr int kWords = D / 32, kChunks = D / 32;
+    constexpr int kTurns = (R * (D / 4) + kNdThreads - 1) / kNdThreads;   // of the threads over a record
+    static_assert(!SPLIT || R <= 4, "the remainders take columns 4-7");
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ int s_last;
+    __shared__ int s_last[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, i = lane & 3;
     const uint32_t sbase = smem_addr(sm);
-    const uint32_t ring = sbase + (uint32_t)warp * L::kStages * L::kBlock;
-    const uint32_t bars = sbase + L::kBars + (uint32_t)warp * L::kStages * 8;
-    if (lane < L::kStages) mbar_init(bars + 8u * lane, 1u);
-    fence_mbar_init();
-    __syncwarp();
+    constexpr uint32_t kToEmpty = 8u * kNdWarps * L::kStages;        // from a stage's full barrier to its empty one
+    const uint32_t bars = sbase + L::kBars;
+    if (tid < kNdWarps * L::kStages) {
+        mbar_init(bars + 8u * tid, kNdSub);
+        mbar_init(bars + kToEmpty + 8u * tid, 1u);
+        fence_mbar_init();
+    }
 
-    // ---- this CTA's range of units
+    // ---- this CTA's range of units, floor(total c / n) of them before CTA c
     NdWalk w;
-    long long total, at0;                                // units of the call; the range's first
+    int each, extra, at0, ctas;                          // total = ctas each + extra; at0: the range's first unit
     {
-        long long* red = reinterpret_cast<long long*>(sm + L::kScan);
-        const int per = (A.n + kNdThreads - 1) / kNdThreads;
-        const int b0 = tid * per, b1 = min(A.n, b0 + per);
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += (long long)nd_span(G, A, b).units * G.hkv;
-        long long pre = mine;
+        int* red = reinterpret_cast<int*>(sm + L::kScan);   // [warps], start [3]
+        long long total = 0, before = 0, mine = 0;
+        w.from = 0;
+        if (A.n <= 32) {                                 // a warp sees all requests: no block-wide scan
+            w.fetch(G, A, lane);
+            mine = (long long)w.mine.units * G.hkv;
+        } else {
+            const int per = (A.n + kNdThreads - 1) / kNdThreads;
+            const int b0 = min(A.n, tid * per), b1 = min(A.n, b0 + per);   // none for the producer warp
+            for (int b = b0; b < b1; ++b) mine += (long long)nd_span(G, A, b).units * G.hkv;
+        }
+        before = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(~0u, pre, o);
-            if (lane >= o) pre += x;
+            const long long x = __shfl_up_sync(~0u, before, o);
+            if (lane >= o) before += x;
         }
-        if (lane == 31) red[warp] = pre;
-        __syncthreads();
-        total = 0;
-        long long before = 0;
+        total = __shfl_sync(~0u, before, 31);
+        before -= mine;
+        long long* sums = reinterpret_cast<long long*>(red);
+        if (A.n > 32) {
+            if (lane == 0 && warp < kNdWarps) sums[warp] = total;
+            __syncthreads();
+            total = 0;
 #pragma unroll
-        for (int k = 0; k < kNdWarps; ++k) {
-            if (k == warp) before = total;
-            total += red[k];
-        }
-        if (total == 0) return;                          // nothing to do, for every CTA
-        const long long n = min((long long)gridDim.x, total);
-        if (blockIdx.x >= n) return;
-        at0 = total * blockIdx.x / n;
-        w.left = (int)(total * (blockIdx.x + 1) / n - at0);
-        pre += before - mine;                            // exclusive
-        int* start = reinterpret_cast<int*>(red + kNdWarps);
-        if (at0 >= pre && at0 < pre + mine) {
-            long long at = at0 - pre;
-            for (int b = b0; b < b1; ++b) {
-                const NdSpan s = nd_span(G, A, b);
-                const long long u = (long long)s.units * G.hkv;
-                if (at < u) {
-                    start[0] = b;
-                    start[1] = (int)(at / s.units);
-                    start[2] = (int)(at % s.units);
-                    break;
-                }
-                at -= u;
+            for (int k = 0; k < kNdWarps; ++k) {
+                if (k == warp) before += total;
+                total += sums[k];
             }
         }
-        __syncthreads();
-        w.b = start[0];
-        w.h = start[1];
-        w.unit = start[2];
-    }
-    w.from = w.b & ~31;
-    w.fetch(G, A, lane);
-    w.take();
-    const long long ctas = min((long long)gridDim.x, total);
-
-    // ---- producer side: the next block to fetch
-    NdWalk p = w;
-    int p_tok, p_end;                                    // this warp's next block of the segment; its end
-    bool p_more = true;
-    auto p_open = [&]() {
-        p_tok = p.base + p.unit * kNdUnit + 16 * warp;
-        p_end = min(p.len, p.base + (p.unit + p.count()) * kNdUnit);
-    };
-    auto p_find = [&]() {                                // to the first segment with a block left for this warp
-        while (p_more && p_tok >= p_end) {
-            p_more = p.next(G, A, lane);
-            if (p_more) p_open();
+        if (total >= (1ll << 31)) {                      // more than this kernel counts
+            if (blockIdx.x == 0 && tid == 0) nib_error(G, 10u /*DWKV_DEV_BAD_LENGTH*/, 0xffffffffu, (uint32_t)(total >> 31));
+            return;
         }
-    };
-    p_open();
-    p_find();
-    int p_id = 0;                                        // page of the block at p_tok
-    auto p_look = [&]() {
-        if (p_more) p_id = __ldg(A.table + (size_t)p.b * G.max_blocks + p_tok / G.page);
-    };
-    p_look();
-    int p_stage = 0;
-    uint32_t holes = 0;                                  // stages whose block lies in no page
-    auto p_issue = [&]() {
-        if (!p_more) return;
-        const uint32_t bar = bars + 8u * p_stage;
-        if ((unsigned)p_id < (unsigned)G.num_pages) {
-            holes &= ~(1u << p_stage);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, L::kBlock);
-                bulk_g2s(ring + (uint32_t)p_stage * L::kBlock, A.pool + nib_block_at(G, p_id, p.h, p_tok % G.page), L::kBlock, bar);
-            }
+        const int n = min((int)gridDim.x, (int)total);   // CTAs with work
+        if ((int)blockIdx.x >= n) return;
+        each = (int)total / n;
+        extra = (int)total - each * n;
+        ctas = n;
+        at0 = each * (int)blockIdx.x + extra * (int)blockIdx.x / n;
+        w.left = each * (int)(blockIdx.x + 1) + extra * (int)(blockIdx.x + 1) / n - at0;
+        const bool here = at0 >= before && at0 < before + mine;
+        if (A.n <= 32) {
+            const uint32_t who = __ballot_sync(~0u, here);
+            w.b = __ffs(who) - 1;
+            w.take();
+            const int at = at0 - (int)__shfl_sync(~0u, before, w.b);
+            w.h = at / w.units;
+            w.unit = at - w.h * w.units;
         } else {
-            holes |= 1u << p_stage;
-            if (lane == 0) {
-                mbar_arrive(bar);
-                nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)p.b, (uint32_t)p_id);
+            int* start = red + 2 * kNdWarps;
+            if (here) {
+                int at = at0 - (int)before;
+                const int per = (A.n + kNdThreads - 1) / kNdThreads;
+                for (int b = tid * per; b < A.n; ++b) {
+                    const NdSpan s = nd_span(G, A, b);
+                    if (at < s.units * G.hkv) {
+                        start[0] = b;
+                        start[1] = at / s.units;
+                        start[2] = at % s.units;
+                        break;
+                    }
+                    at -= s.units * G.hkv;
+                }
+            }
+            __syncthreads();
+            w.b = start[0];
+            w.h = start[1];
+            w.unit = start[2];
+            w.from = w.b & ~31;
+            w.fetch(G, A, lane);
+            w.take();
+        }
+    }
+    __syncthreads();                                     // the mbarriers are ready
+    // The CTA that has unit u.
+    auto cta_of = [&](int u) {
+        return (int)((((long long)u + 1) * ctas - 1) / ((long long)each * ctas + extra));
+    };
+
+    // ---- producer: lane 2 w + k keeps block k of warp w's stages filled
+    if (warp == kNdWarps) {
+        const int cw = min(lane / kNdSub, kNdWarps - 1), sub = lane % kNdSub;
+        const uint32_t ring = bars + 8u * cw * L::kStages;
+        int stage = 0, rounds = 0;
+        bool ok = true;
+        for (bool some = true; ok && some; some = w.next(G, A, lane)) {
+            const int cnt = lane < kNdBlocks ? w.count() : 0;
+            const int end = min(w.len, w.base + (w.unit + w.count()) * kNdUnit);
+            const int inner_hi = w.len - w.nq;           // tokens up to here are seen by every row,
+            const int inner_lo = G.window > 0 ? w.len - G.window : 0;   // and from here on
+            const int32_t* row = A.table + (size_t)w.b * G.max_blocks;
+            int t = w.base + w.unit * kNdUnit + 16 * lane, u = 0;
+            int id = cnt > 0 && t < end ? __ldg(row + (t >> G.page_shift)) : -1;
+            uint32_t idle = 0;
+            uint64_t since = 0;
+            while (__any_sync(~0u, u < cnt)) {
+                // a full turn of polls without a copy is timed
+                const bool go = u < cnt && (rounds == 0 || mbar_poll(ring + kToEmpty + 8u * stage, (uint32_t)(rounds - 1) & 1u));
+                if (__any_sync(~0u, go)) {
+                    idle = 0;
+                } else if ((++idle & 63u) == 0u) {
+                    if (idle == 64u) since = global_ns();
+                    if (__any_sync(~0u, global_ns() - since > kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (go) {
+                    const bool there = t < end, good = there && (unsigned)id < (unsigned)G.num_pages;
+                    if (there && !good) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)w.b, (uint32_t)id);
+                    sm[L::kFlags + (cw * L::kStages + stage) * kNdSub + sub] = (uint8_t)((good ? 0 : 1) | (t + 15 > inner_hi || t < inner_lo ? 2 : 0));
+                    if (good) {
+                        mbar_arrive_expect_tx(ring + 8u * stage, L::kBlock);
+                        bulk_g2s(sbase + (uint32_t)((cw * L::kStages + stage) * kNdSub + sub) * L::kBlock,
+                                 A.pool + nib_block_at(G, id, w.h, t & (G.page - 1)), L::kBlock, ring + 8u * stage);
+                    } else {
+                        mbar_arrive(ring + 8u * stage);
+                    }
+                    if (++stage == L::kStages) {
+                        stage = 0;
+                        ++rounds;
+                    }
+                    t += kNdUnit;
+                    ++u;
+                    if (u < cnt && t < end) id = __ldg(row + (t >> G.page_shift));
+                }
             }
         }
-        p_stage = p_stage + 1 == L::kStages ? 0 : p_stage + 1;
-        p_tok += kNdUnit;
-        p_find();
-        p_look();
-    };
-    for (int s = 0; s < L::kStages; ++s) p_issue();
+        if (!ok) {                                       // the copies in flight end first, each wait with a limit
+            if (lane == 0) nib_error(G, 6u /*DWKV_DEV_TIMEOUT*/, 0x6e70u, (uint32_t)w.b);
+            for (int k = 0; k < L::kStages; ++k)
+                if (rounds > 0 || k < stage) mbar_wait_for(ring + 8u * k, (uint32_t)(rounds - (k >= stage)) & 1u, 10000000ull);
+        }
+        return;
+    }
 
     // ---- consumer side
-    int c_stage = 0;
-    uint32_t c_phase = 0;
-    bool dead = false;                                   // a wait ran out: leave out what is left
-    long long at = at0;
-    const uint32_t vrow = (uint32_t)(lane & 7) + (uint32_t)((lane >> 3) & 1) * 8u;
+    const uint32_t c_ring = bars + 8u * warp * L::kStages;
+    uint32_t c_stage = 0, c_phase = 0;
+    const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
+    bool dead = false;                                   // a wait ran out: what is left is left out
+    int at = at0;
+    // ldmatrix row of this lane: token vrow, 16-byte chunk 0 or 1; chunks 2 and 3 are 32 bytes away, by xor
+    const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+    const uint32_t vaddr = 9u * D + (uint32_t)vrow * (D / 2) + (uint32_t)nib_vchunk(D, vrow, lane >> 4) * 16u;
     for (bool more = true; more; more = w.next(G, A, lane)) {
         const int cnt = w.count(), rows = w.nq * G.g;
         const int row0 = A.cu[w.b];
         // queries as B fragments, each row scaled by a power of two to below 2 (exact in fp16)
-        uint32_t qf[NT][kKs][2];
-        float fac[NT][2];                                // score -> log2 units, for the lane's columns
+        uint4* qs = reinterpret_cast<uint4*>(sm + L::kQ) + lane;
+        float fac[NT][2];                                // unscaled score -> log2 units, for the lane's columns
         int pos[NT][2];                                  // position of the lane's columns' rows
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -305,10 +385,9 @@ __global__ void __launch_bounds__(kNdThreads, NdLayout<D, NT>::kCtas) nib_decode
                     f[2 * y] = (FP16 ? half_lo(raw[x][y]) : bf16lo(raw[x][y])) * sc;
                     f[2 * y + 1] = (FP16 ? half_hi(raw[x][y]) : bf16hi(raw[x][y])) * sc;
                 }
-                qf[nt][2 * x][0] = pack_half2(f[0], f[4]);
-                qf[nt][2 * x][1] = pack_half2(f[1], f[5]);
-                qf[nt][2 * x + 1][0] = pack_half2(f[2], f[6]);
-                qf[nt][2 * x + 1][1] = pack_half2(f[3], f[7]);
+                if (warp == 0)                           // every warp has the same; one writes
+                    qs[(nt * kWords + x) * 32] = make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]),
+                                                            pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
             }
             const float mult = G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23);
             fac[nt][0] = __shfl_sync(~0u, mult, 8 * i);
@@ -319,100 +398,113 @@ __global__ void __launch_bounds__(kNdThreads, NdLayout<D, NT>::kCtas) nib_decode
                 pos[nt][c] = w.len - w.nq + min(col, rows - 1) / G.g;
             }
         }
-        float m[NT][2], l[NT][2], o[NT][2 * kChunks][4];
+        float m[NT][2], thr[NT][2], l[NT][2], o[NT][2 * kChunks][4];   // thr: the unscaled score that moves m
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = kNdNone;
+            thr[nt][0] = thr[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int x = 0; x < 2 * kChunks; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
         }
-        const int end = min(w.len, w.base + (w.unit + cnt) * kNdUnit);
-        const int inner_hi = w.len - w.nq;               // tokens up to here are seen by every row
-        const int inner_lo = G.window > 0 ? w.len - G.window : 0;
-        for (int t0 = w.base + w.unit * kNdUnit + 16 * warp; t0 < end; t0 += kNdUnit) {
-            if (!dead && !mbar_wait(bars + 8u * c_stage, c_phase)) {
+        named_barrier(1, kNdThreads);
+        int t0 = w.base + w.unit * kNdUnit + kNdSub * 16 * warp;
+        for (int u = 0; u < cnt; ++u, t0 += kNdUnit) {
+            const uint32_t at_s = warp * L::kStages + c_stage, c_off = at_s * L::kStage;
+            if (!dead && !mbar_wait(c_ring + 8u * c_stage, c_phase)) {
                 dead = true;
                 if (lane == 0) nib_error(G, 6u /*DWKV_DEV_TIMEOUT*/, 0x6e64u, (uint32_t)w.b);
-                for (int k = 1; k < L::kStages; ++k) {   // the other copies in flight, each with a limit
-                    const int st = (c_stage + k) % L::kStages;
-                    mbar_wait_for(bars + 8u * st, c_phase ^ (uint32_t)(c_stage + k >= L::kStages), 10000000ull);
-                }
             }
-            const uint8_t* blk = sm + (size_t)(warp * L::kStages + c_stage) * L::kBlock;
-            const uint32_t blk_s = ring + (uint32_t)c_stage * L::kBlock;
-            if (!dead && !((holes >> c_stage) & 1u)) {
-                const bool edge = t0 + 15 > inner_hi || t0 < inner_lo;
-                // ---- scores of 16 tokens
-                uint32_t kw[2][kWords];
-                uint32_t ksc[2];
-                if (D == 128) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(blk + g * 64 + i * 16);
-                    const uint4 b = *reinterpret_cast<const uint4*>(blk + (g + 8) * 64 + i * 16);
-                    kw[0][0] = a.x; kw[0][1] = a.y; kw[0][kWords - 2] = a.z; kw[0][kWords - 1] = a.w;
-                    kw[1][0] = b.x; kw[1][1] = b.y; kw[1][kWords - 2] = b.z; kw[1][kWords - 1] = b.w;
-                    ksc[0] = *reinterpret_cast<const uint16_t*>(blk + 8 * D + g * 8 + 2 * i);
-                    ksc[1] = *reinterpret_cast<const uint16_t*>(blk + 8 * D + (g + 8) * 8 + 2 * i);
-                } else {
-                    const uint2 a = *reinterpret_cast<const uint2*>(blk + g * 32 + i * 8);
-                    const uint2 b = *reinterpret_cast<const uint2*>(blk + (g + 8) * 32 + i * 8);
-                    kw[0][0] = a.x; kw[0][1] = a.y;
-                    kw[1][0] = b.x; kw[1][1] = b.y;
-                    ksc[0] = blk[8 * D + g * 4 + i];
-                    ksc[1] = blk[8 * D + (g + 8) * 4 + i];
-                }
-                float s[NT][4], s2[NT][4];
+            const uint32_t flag = *reinterpret_cast<const uint16_t*>(sm + L::kFlags + kNdSub * at_s);
+            if (!dead && (flag & 0x101u) != 0x101u) {
+                const bool edge = flag;                  // a block not there, or not seen whole by every row
+                // ---- scores of 32 tokens
+                float s[kNdSub][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) s[nt][x] = s2[nt][x] = 0.f;
-#pragma unroll
-                for (int grp = 0; grp < kWords / 2; ++grp) {     // 16 channels of the lane share a scale
-                    uint32_t r[2], b0[2], b1[2];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        r[z] = __byte_perm(ksc[z], 0, grp ? 0x1414 : 0x0404) >> 1;
-                        b0[z] = hmul2_(r[z], kNibB0);
-                        b1[z] = hmul2_(r[z], kNibB1);
+                for (int k = 0; k < kNdSub; ++k) {
+                    const uint8_t* blk = sm + c_off + k * L::kBlock;
+                    uint32_t kw[2][kWords];
+                    if (D == 128) {
+                        const uint4 a = *reinterpret_cast<const uint4*>(blk + g * 64 + i * 16);
+                        const uint4 b = *reinterpret_cast<const uint4*>(blk + (g + 8) * 64 + i * 16);
+                        kw[0][0] = a.x; kw[0][1] = a.y; kw[0][kWords - 2] = a.z; kw[0][kWords - 1] = a.w;
+                        kw[1][0] = b.x; kw[1][1] = b.y; kw[1][kWords - 2] = b.z; kw[1][kWords - 1] = b.w;
+                    } else {
+                        const uint2 a = *reinterpret_cast<const uint2*>(blk + g * 32 + i * 8);
+                        const uint2 b = *reinterpret_cast<const uint2*>(blk + (g + 8) * 32 + i * 8);
+                        kw[0][0] = a.x; kw[0][1] = a.y;
+                        kw[1][0] = b.x; kw[1][1] = b.y;
                     }
+                    float s2[NT][4];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int x = 2 * grp + y;
-                        uint32_t u0[4], u1[4];
-                        nib_unpack(kw[0][x], r[0], b0[0], b1[0], u0);
-                        nib_unpack(kw[1][x], r[1], b0[1], b1[1], u1);
-                        const uint32_t a0[4] = {u0[0], u1[0], u0[1], u1[1]}, a1[4] = {u0[2], u1[2], u0[3], u1[3]};
+                    for (int grp = 0; grp < kWords / 2; ++grp) {     // 16 channels of the lane share a scale
+                        uint32_t r[2], b0[2], b1[2];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(s[nt], a0, qf[nt][2 * x]);
-                            mma_f16(s2[nt], a1, qf[nt][2 * x + 1]);
+                        for (int z = 0; z < 2; ++z) {
+                            // the scale byte << 7 in both halves
+                            r[z] = 0x00800080u * blk[8 * D + (g + 8 * z) * (D / 16) + i * (D / 64) + grp];
+                            b0[z] = hmul2_(r[z], kNibB0);
+                            b1[z] = hmul2_(r[z], kNibB1);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int x = 2 * grp + y;
+                            uint32_t u0[4], u1[4];
+                            nib_unpack(kw[0][x], r[0], b0[0], b1[0], e8, eh, u0);
+                            nib_unpack(kw[1][x], r[1], b0[1], b1[1], e8, eh, u1);
+                            const uint32_t a0[4] = {u0[0], u1[0], u0[1], u1[1]}, a1[4] = {u0[2], u1[2], u0[3], u1[3]};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint4 q = qs[(nt * kWords + x) * 32];
+                                const uint32_t q0[2] = {q.x, q.y}, q1[2] = {q.z, q.w};
+                                if (x == 0) {
+                                    mma_f16_first(s[k][nt], a0, q0);
+                                    mma_f16_first(s2[nt], a1, q1);
+                                } else {
+                                    mma_f16(s[k][nt], a0, q0);
+                                    mma_f16(s2[nt], a1, q1);
+                                }
+                            }
                         }
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[k][nt][x] += s2[nt][x];
+                }
+                if (edge) {                              // the volatile keeps this a branch: few blocks take it
+                    asm volatile("" ::: "memory");
+#pragma unroll
+                    for (int k = 0; k < kNdSub; ++k)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int t = t0 + 16 * k + g + 8 * (x >> 1), hi = pos[nt][x & 1];
+                                if ((flag >> 8 * k & 1u) || t > hi || (G.window > 0 && t <= hi - G.window)) s[k][nt][x] = -INFINITY;
+                            }
                 }
                 bool jump = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int k = 0; k < kNdSub; ++k)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        s[nt][x] = (s[nt][x] + s2[nt][x]) * fac[nt][x & 1];
-                        if (edge) {
-                            const int t = t0 + g + 8 * (x >> 1), hi = pos[nt][x & 1];
-                            if (t > hi || (G.window > 0 && t <= hi - G.window)) s[nt][x] = -INFINITY;
-                        }
-                        jump |= s[nt][x] > m[nt][x & 1] + kNdLag;
-                    }
-                }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) jump |= s[k][nt][x] > thr[nt][x & 1];
                 if (__any_sync(~0u, jump)) {             // the maximum moves: all rows take the new one
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float x = fmaxf(m[nt][c], fmaxf(s[nt][c], s[nt][c + 2]));
+                            float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+#pragma unroll
+                            for (int k = 1; k < kNdSub; ++k) x = fmaxf(x, fmaxf(s[k][nt][c], s[k][nt][c + 2]));
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                            x = fmaxf(m[nt][c], fac[nt][c] * fmaxf(x, __shfl_xor_sync(~0u, x, 16)));
                             const float f = ex2(m[nt][c] - x);
                             m[nt][c] = x;
+                            thr[nt][c] = x > kNdNone ? (x + kNdLag) / fac[nt][c] : -INFINITY;
                             l[nt][c] *= f;
 #pragma unroll
                             for (int y = 0; y < 2 * kChunks; ++y) {
@@ -421,71 +513,77 @@ __global__ void __launch_bounds__(kNdThreads, NdLayout<D, NT>::kCtas) nib_decode
                             }
                         }
                 }
-                uint32_t pf[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float pr[4];
+                for (int k = 0; k < kNdSub; ++k) {
+                    uint32_t pf[NT][2];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        pr[x] = ex2(s[nt][x] - (m[nt][x & 1] - kNdBias));
-                        l[nt][x & 1] += pr[x];
-                    }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float pr[4];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        uint32_t h = pack_half2(pr[2 * z], pr[2 * z + 1]);
-                        if (SPLIT) {                     // columns 4-7: what the rounding left
-                            const uint32_t rest = pack_half2(pr[2 * z] - half_lo(h), pr[2 * z + 1] - half_hi(h));
-                            h = i >= 2 ? rest : h;
+                        for (int x = 0; x < 4; ++x) {
+                            pr[x] = ex2(fmaf(s[k][nt][x], fac[nt][x & 1], kNdBias - m[nt][x & 1]));
+                            l[nt][x & 1] += pr[x];
                         }
-                        pf[nt][z] = movm_t(h);
-                    }
-                }
-                // ---- values: O^T += V^T P^T
-                uint32_t vs[kChunks];
-                if (D == 128) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(blk + 17 * D + ((g >> 2) * 4 + i) * 16);
-                    vs[0] = v.x; vs[1] = v.y; vs[kChunks - 2] = v.z; vs[kChunks - 1] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(blk + 17 * D + ((g >> 2) * 4 + i) * 8);
-                    vs[0] = v.x; vs[1] = v.y;
-                }
-                if (t0 + 16 > w.len) {                   // bytes behind the last token are not to be believed
-                    const int t = t0 + 2 * i;
-                    uint32_t keep = 0;
-                    if (t < w.len) keep |= 0xffu;
-                    if (t + 1 < w.len) keep |= 0xff00u;
-                    if (t + 8 < w.len) keep |= 0xff0000u;
-                    if (t + 9 < w.len) keep |= 0xff000000u;
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) vs[c] &= keep;
-                }
-#pragma unroll
-                for (int c2 = 0; c2 < kChunks; c2 += 2) {
-                    uint32_t v[4];
-                    const int chunk = nib_vchunk(D, (int)vrow, c2 + (lane >> 4));
-                    ldsm_x4_t(blk_s + 9u * D + vrow * (D / 2) + (uint32_t)chunk * 16u, v);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int c = c2 + y;
-                        uint32_t u[2][4];
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const uint32_t r = __byte_perm(vs[c], 0, z ? 0x3424 : 0x1404) >> 1;
-                            nib_unpack(v[2 * y + z], r, hmul2_(r, kNibB0), hmul2_(r, kNibB1), u[z]);
+                            uint32_t h = pack_half2(pr[2 * z], pr[2 * z + 1]);
+                            if (SPLIT) {                 // columns 4-7: what the rounding left
+                                const uint32_t rest = pack_half2(pr[2 * z] - half_lo(h), pr[2 * z + 1] - half_hi(h));
+                                h = i >= 2 ? rest : h;
+                            }
+                            pf[nt][z] = movm_t(h);
                         }
+                    }
+                    // ---- values: O^T += V^T P^T
+                    const uint8_t* blk = sm + c_off + k * L::kBlock;
+                    uint32_t vs[kChunks];
+                    if (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(blk + 17 * D + ((g >> 2) * 4 + i) * 16);
+                        vs[0] = v.x; vs[1] = v.y; vs[kChunks - 2] = v.z; vs[kChunks - 1] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(blk + 17 * D + ((g >> 2) * 4 + i) * 8);
+                        vs[0] = v.x; vs[1] = v.y;
+                    }
+                    if (edge) {                          // bytes behind the last token are not to be believed
+                        asm volatile("" ::: "memory");
+                        const int t = t0 + 16 * k + 2 * i, len = flag >> 8 * k & 1u ? 0 : w.len;
+                        uint32_t keep = 0;
+                        if (t < len) keep |= 0xffu;
+                        if (t + 1 < len) keep |= 0xff00u;
+                        if (t + 8 < len) keep |= 0xff0000u;
+                        if (t + 9 < len) keep |= 0xff000000u;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t a[4] = {u[0][2 * e], u[0][2 * e + 1], u[1][2 * e], u[1][2 * e + 1]};
+                        for (int c = 0; c < kChunks; ++c) vs[c] &= keep;
+                    }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * c + e], a, pf[nt]);
+                    for (int c2 = 0; c2 < kChunks; c2 += 2) {
+                        uint32_t v[4];
+                        ldsm_x4_t(sbase + c_off + k * L::kBlock + (vaddr ^ (uint32_t)(c2 * 16)), v);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int c = c2 + y;
+                            uint32_t u[2][4];
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t r = __byte_perm(vs[c], 0, z ? 0x3424 : 0x1404) >> 1;
+                                nib_unpack(v[2 * y + z], r, hmul2_(r, kNibB0), hmul2_(r, kNibB1), e8, eh, u[z]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t a[4] = {u[0][2 * e], u[0][2 * e + 1], u[1][2 * e], u[1][2 * e + 1]};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * c + e], a, pf[nt]);
+                            }
                         }
                     }
                 }
             }
-            __syncwarp();                                // the block is read: its stage takes the next one
-            c_stage = c_stage + 1 == L::kStages ? 0 : c_stage + 1;
-            if (c_stage == 0) c_phase ^= 1u;
-            if (!dead) p_issue();
+            __syncwarp();                                // the blocks are read: their stage takes another unit
+            if (lane == 0 && !dead) mbar_arrive(c_ring + kToEmpty + 8u * c_stage);
+            if (++c_stage == L::kStages) {
+                c_stage = 0;
+                c_phase ^= 1u;
+            }
         }
 
         // ---- the segment ends: merge the warps
@@ -500,97 +598,161 @@ __global__ void __launch_bounds__(kNdThreads, NdLayout<D, NT>::kCtas) nib_decode
                 x += __shfl_xor_sync(~0u, x, 8);
                 x += __shfl_xor_sync(~0u, x, 16);
                 if (g == 0) {
-                    ml[warp * 8 * NT + nt * 8 + 2 * i + c] = m[nt][c];
-                    ml[(kNdWarps + warp) * 8 * NT + nt * 8 + 2 * i + c] = x;
+                    ml[warp * 16 + nt * 8 + 2 * i + c] = m[nt][c];
+                    ml[(kNdWarps + warp) * 16 + nt * 8 + 2 * i + c] = x;
                 }
             }
         const bool whole = w.unit == 0 && cnt == w.units;
-        const long long first = at - w.unit;             // unit 0 of this (request, kv-head)
-        const int c0 = (int)(((first + 1) * ctas - 1) / total), c1 = (int)(((first + w.units) * ctas - 1) / total);
-        float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * nd_record_floats<D>(R);
+        const int first = at - w.unit;                   // unit 0 of this (request, kv-head)
+        float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * (R * (D + 2));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (nt) __syncthreads();                     // the merge rows are free again
+            if (nt) named_barrier(1, kNdThreads);        // the merge rows are free again
             if (SPLIT) {                                 // the remainders' products join their rows
 #pragma unroll
                 for (int y = 0; y < 2 * kChunks; ++y)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[nt][y][x] += __shfl_xor_sync(~0u, o[nt][y][x], 2);
             }
-            if (!SPLIT || i < 2) {
+            if (R > 4 || i < 2) {
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        *reinterpret_cast<float4*>(mo + (size_t)(warp * 8 + 2 * i + y) * L::kPitch + 32 * c + 4 * g) =
+                        *reinterpret_cast<float4*>(mo + (size_t)(warp * L::kMr + 2 * i + y) * L::kPitch + 32 * c + 4 * g) =
                             make_float4(o[nt][2 * c][y], o[nt][2 * c][y + 2], o[nt][2 * c + 1][y], o[nt][2 * c + 1][y + 2]);
             }
-            __syncthreads();
-            const int r_hi = min(rows - 8 * nt, SPLIT ? 4 : 8);
+            named_barrier(1, kNdThreads);
+            const int r_hi = min(rows - 8 * nt, L::kMr);
             for (int e = tid; e < r_hi * (D / 4); e += kNdThreads) {
                 const int r = e / (D / 4), ch = e % (D / 4) * 4;
                 float mm = kNdNone;
 #pragma unroll
-                for (int k = 0; k < kNdWarps; ++k) mm = fmaxf(mm, ml[k * 8 * NT + nt * 8 + r]);
+                for (int k = 0; k < kNdWarps; ++k) mm = fmaxf(mm, ml[k * 16 + nt * 8 + r]);
                 float ll = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < kNdWarps; ++k) {
-                    const float f = ex2(ml[k * 8 * NT + nt * 8 + r] - mm);
-                    const float4 v = *reinterpret_cast<const float4*>(mo + (size_t)(k * 8 + r) * L::kPitch + ch);
-                    ll = fmaf(f, ml[(kNdWarps + k) * 8 * NT + nt * 8 + r], ll);
+                    const float f = ex2(ml[k * 16 + nt * 8 + r] - mm);
+                    const float4 v = *reinterpret_cast<const float4*>(mo + (size_t)(k * L::kMr + r) * L::kPitch + ch);
+                    ll = fmaf(f, ml[(kNdWarps + k) * 16 + nt * 8 + r], ll);
                     acc.x = fmaf(f, v.x, acc.x);
                     acc.y = fmaf(f, v.y, acc.y);
                     acc.z = fmaf(f, v.z, acc.z);
                     acc.w = fmaf(f, v.w, acc.w);
                 }
+                const int rr = nt * 8 + r;
                 if (whole) {
-                    nib_put<FP16>(G, A, row0, w.h, nt * 8 + r, D, ch, mm, ll, acc);
+                    nib_put<FP16>(G, A, row0, w.h, rr, D, ch, mm, ll, acc);
                 } else {
-                    const int rr = nt * 8 + r;
                     if (ch == 0) { rec[rr] = mm; rec[R + rr] = ll; }
                     *reinterpret_cast<float4*>(rec + 2 * R + (size_t)rr * D + ch) = acc;
                 }
             }
         }
         if (!whole) {                                    // the last CTA of this (request, kv-head) merges the records
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int n = c1 - c0 + 1;
+            named_barrier(1, kNdThreads);
+            if (tid == 0) {                              // the barrier, then one fence: the whole CTA's record is out
+                __threadfence();
+                const int c0 = cta_of(first), c1 = cta_of(first + w.units - 1);
                 const int k = atomicAdd(A.tickets + c0, 1);
-                s_last = k == n - 1;
-                if (s_last) {
-                    A.tickets[c0] = 0;
-                    __threadfence();
-                }
+                s_last[0] = k == c1 - c0;
+                s_last[1] = c0;
+                s_last[2] = c1;
+                if (k == c1 - c0) A.tickets[c0] = 0;
+                __threadfence();
             }
-            __syncthreads();
-            if (s_last) {
-                const int first_slot = first == total * c0 / ctas ? 0 : 1;
-                for (int e = tid; e < rows * (D / 4); e += kNdThreads) {
-                    const int r = e / (D / 4), ch = e % (D / 4) * 4;
-                    float mm = kNdNone;
-                    for (int c = c0; c <= c1; ++c)
-                        mm = fmaxf(mm, __ldcg(A.records + (size_t)(2 * c + (c == c0 ? first_slot : 0)) * nd_record_floats<D>(R) + r));
-                    float ll = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* x = A.records + (size_t)(2 * c + (c == c0 ? first_slot : 0)) * nd_record_floats<D>(R);
-                        const float f = ex2(__ldcg(x + r) - mm);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(x + 2 * R + (size_t)r * D + ch));
-                        ll = fmaf(f, __ldcg(x + R + r), ll);
-                        acc.x = fmaf(f, v.x, acc.x);
-                        acc.y = fmaf(f, v.y, acc.y);
-                        acc.z = fmaf(f, v.z, acc.z);
-                        acc.w = fmaf(f, v.w, acc.w);
+            named_barrier(1, kNdThreads);
+            if (s_last[0]) {
+                // Each record's share of each row first (its maximum against the common one, in shared
+                // memory, kShares records at a time), then groups of rows D / 4 threads take every
+                // groups-th record, four channels of a row a thread; the groups' sums meet at the end.
+                constexpr int kRec = R * (D + 2), kShares = 64;
+                const int c0 = s_last[1], c1 = s_last[2];
+                const int slot0 = first == each * c0 + extra * c0 / ctas ? 0 : 1;   // the first CTA's record; the others' are at 0
+                const float* recs = A.records + (size_t)(2 * c0 + slot0) * kRec;
+                auto record = [&](int c) { return c == c0 ? recs : A.records + (size_t)(2 * c) * kRec; };
+                float* sh = reinterpret_cast<float*>(sm + L::kMerge);           // [kShares][R] shares
+                float* top = reinterpret_cast<float*>(sm + L::kMl);             // [R] maximum, [R] sum
+                const int items = rows * (D / 4), groups = max(1, kNdThreads / items);
+                const int grp = items < kNdThreads ? tid / items : 0;
+                float4 acc[kTurns];
+#pragma unroll
+                for (int k = 0; k < kTurns; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (tid < R) {
+                    top[tid] = kNdNone;
+                    top[R + tid] = 0.f;
+                }
+                named_barrier(1, kNdThreads);
+                for (int cb = c0; cb <= c1; cb += kShares) {
+                    const int nc = min(kShares, c1 - cb + 1);
+                    // a warp a row: the maximum over the records so far, shares against it
+                    for (int r = warp; r < rows; r += kNdWarps) {
+                        const bool a1 = lane < nc, a2 = lane + 32 < nc;
+                        const float* x1 = record(cb + (a1 ? lane : 0));
+                        const float* x2 = record(cb + (a2 ? lane + 32 : 0));
+                        const float m1 = a1 ? __ldcg(x1 + r) : kNdNone, m2 = a2 ? __ldcg(x2 + r) : kNdNone;
+                        const float l1 = a1 ? __ldcg(x1 + R + r) : 0.f, l2 = a2 ? __ldcg(x2 + R + r) : 0.f;
+                        float mm = fmaxf(m1, m2);
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+                        const float was = top[r];
+                        mm = fmaxf(mm, was);
+                        const float f1 = a1 ? ex2(m1 - mm) : 0.f, f2 = a2 ? ex2(m2 - mm) : 0.f;
+                        float ll = f1 * l1 + f2 * l2;
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(~0u, ll, o);
+                        sh[lane * R + r] = f1;
+                        sh[(lane + 32) * R + r] = f2;
+                        __syncwarp();
+                        if (lane == 0) {
+                            const float f0 = ex2(was - mm);
+                            top[r] = mm;
+                            top[R + r] = fmaf(top[R + r], f0, ll);
+                            sh[kShares * R + r] = f0;    // what was summed before
+                        }
                     }
-                    nib_put<FP16>(G, A, row0, w.h, r, D, ch, mm, ll, acc);
+                    named_barrier(1, kNdThreads);
+#pragma unroll
+                    for (int k = 0; k < kTurns; ++k) {
+                        const int e = (items < kNdThreads ? tid % items : tid) + k * kNdThreads;
+                        if (e >= items || grp >= groups) continue;
+                        const int r = e / (D / 4), ch = e % (D / 4) * 4;
+                        const float f0 = sh[kShares * R + r];
+                        acc[k].x *= f0; acc[k].y *= f0; acc[k].z *= f0; acc[k].w *= f0;
+#pragma unroll 8
+                        for (int c = grp; c < nc; c += groups) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(record(cb + c) + 2 * R + (size_t)r * D + ch));
+                            const float f = sh[c * R + r];
+                            acc[k].x = fmaf(f, v.x, acc[k].x);
+                            acc[k].y = fmaf(f, v.y, acc[k].y);
+                            acc[k].z = fmaf(f, v.z, acc[k].z);
+                            acc[k].w = fmaf(f, v.w, acc[k].w);
+                        }
+                    }
+                    named_barrier(1, kNdThreads);        // the shares are read
+                }
+                if (groups > 1) {                        // items < threads: one turn
+                    float4* part = reinterpret_cast<float4*>(sm + L::kMerge);
+                    part[tid] = acc[0];
+                    named_barrier(1, kNdThreads);
+                    if (tid < items)
+                        for (int k = 1; k < groups; ++k) {
+                            const float4 v = part[tid + k * items];
+                            acc[0].x += v.x; acc[0].y += v.y; acc[0].z += v.z; acc[0].w += v.w;
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < kTurns; ++k) {
+                    const int e = tid + k * kNdThreads;
+                    if (e < items) {
+                        const int r = e / (D / 4), ch = e % (D / 4) * 4;
+                        nib_put<FP16>(G, A, row0, w.h, r, D, ch, top[r], top[R + r], acc[k]);
+                    }
                 }
             }
         }
-        __syncthreads();                                 // the merge rows are free for the next segment
+        named_barrier(1, kNdThreads);                    // the merge rows are free for the next segment
         at += cnt;
     }
 }

@@ -125,16 +125,20 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
 
+// Empty units counted behind each (request, kv-head): what its end costs a CTA (merging the warps,
+// writing, the next one's queries) in units, so that ranges with an end in them carry less.
+constexpr int kNdBorder = 1;
+
 // Where a request's tokens start and how many units they are (none where it has no rows).
 struct NdSpan {
-    int len, nq, base, units;
+    int len, nq, base, units;                            // units: of one kv-head, kNdBorder of them empty
 };
 __device__ __forceinline__ NdSpan nd_span(const NibGeom& G, const NibAttend& A, int b) {
     NdSpan s{0, 0, 0, 0};
     if (b >= A.n) return s;
     if (!nib_request(G, A, b, s.len, s.nq) || s.nq == 0 || s.nq * G.g > A.rows_hi) { s.nq = 0; return s; }
     s.base = G.window > 0 ? max(0, s.len - s.nq - G.window + 1) & ~15 : 0;
-    s.units = max(1, (s.len - s.base + kNdUnit - 1) / kNdUnit);
+    s.units = max(1, (s.len - s.base + kNdUnit - 1) / kNdUnit) + kNdBorder;
     return s;
 }
 
@@ -154,10 +158,11 @@ struct NdWalk {
         base = __shfl_sync(~0u, mine.base, l);
         units = __shfl_sync(~0u, mine.units, l);
     }
-    __device__ __forceinline__ int count() const { return min(left, units - unit); }   // units of this segment
+    __device__ __forceinline__ int real() const { return units - kNdBorder; }
+    __device__ __forceinline__ int count() const { return min(left, real() - unit); }   // units of this segment
     // To the next segment; false at the end of the range.
     __device__ __forceinline__ bool next(const NibGeom& G, const NibAttend& A, int lane) {
-        left -= count();
+        left -= min(left, units - unit);
         if (left <= 0) return false;
         unit = 0;
         if (++h < G.hkv) return true;
@@ -184,7 +189,6 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
     using L = NdLayout<D, R>;
     constexpr int NT = R > 8 ? 2 : 1;                    // MMA column tiles
     constexpr int kWords = D / 32, kChunks = D / 32;
-    constexpr int kTurns = (R * (D / 4) + kNdThreads - 1) / kNdThreads;   // of the threads over a record
     static_assert(!SPLIT || R <= 4, "the remainders take columns 4-7");
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ int s_last[3];
@@ -282,6 +286,12 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
         return (int)((((long long)u + 1) * ctas - 1) / ((long long)each * ctas + extra));
     };
 
+    int at = at0;                                        // the unit at which the walk stands
+    if (w.unit >= w.real()) {                            // the range starts in the empty units behind a kv-head
+        at += min(w.left, w.units - w.unit);
+        if (!w.next(G, A, lane)) return;
+    }
+
     // ---- producer: lane 2 w + k keeps block k of warp w's stages filled
     if (warp == kNdWarps) {
         const int cw = min(lane / kNdSub, kNdWarps - 1), sub = lane % kNdSub;
@@ -344,7 +354,6 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
     uint32_t c_stage = 0, c_phase = 0;
     const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
     bool dead = false;                                   // a wait ran out: what is left is left out
-    int at = at0;
     // ldmatrix row of this lane: token vrow, 16-byte chunk 0 or 1; chunks 2 and 3 are 32 bytes away, by xor
     const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
     const uint32_t vaddr = 9u * D + (uint32_t)vrow * (D / 2) + (uint32_t)nib_vchunk(D, vrow, lane >> 4) * 16u;
@@ -602,8 +611,31 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                     ml[(kNdWarps + warp) * 16 + nt * 8 + 2 * i + c] = x;
                 }
             }
-        const bool whole = w.unit == 0 && cnt == w.units;
+        const bool whole = w.unit == 0 && cnt == w.real();
         const int first = at - w.unit;                   // unit 0 of this (request, kv-head)
+        // Sums the warps' rows of a column tile against their common maximum: put(row, channel, m, l, o).
+        auto merge = [&](int nt, auto put) {
+            const int r_hi = min(rows - 8 * nt, L::kMr);
+            for (int e = tid; e < r_hi * (D / 4); e += kNdThreads) {
+                const int r = e / (D / 4), ch = e % (D / 4) * 4;
+                float mm = kNdNone;
+#pragma unroll
+                for (int k = 0; k < kNdWarps; ++k) mm = fmaxf(mm, ml[k * 16 + nt * 8 + r]);
+                float ll = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kNdWarps; ++k) {
+                    const float f = ex2(ml[k * 16 + nt * 8 + r] - mm);
+                    const float4 v = *reinterpret_cast<const float4*>(mo + (size_t)(k * L::kMr + r) * L::kPitch + ch);
+                    ll = fmaf(f, ml[(kNdWarps + k) * 16 + nt * 8 + r], ll);
+                    acc.x = fmaf(f, v.x, acc.x);
+                    acc.y = fmaf(f, v.y, acc.y);
+                    acc.z = fmaf(f, v.z, acc.z);
+                    acc.w = fmaf(f, v.w, acc.w);
+                }
+                put(nt * 8 + r, ch, mm, ll, acc);
+            }
+        };
         float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * (R * (D + 2));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -623,38 +655,20 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                             make_float4(o[nt][2 * c][y], o[nt][2 * c][y + 2], o[nt][2 * c + 1][y], o[nt][2 * c + 1][y + 2]);
             }
             named_barrier(1, kNdThreads);
-            const int r_hi = min(rows - 8 * nt, L::kMr);
-            for (int e = tid; e < r_hi * (D / 4); e += kNdThreads) {
-                const int r = e / (D / 4), ch = e % (D / 4) * 4;
-                float mm = kNdNone;
-#pragma unroll
-                for (int k = 0; k < kNdWarps; ++k) mm = fmaxf(mm, ml[k * 16 + nt * 8 + r]);
-                float ll = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kNdWarps; ++k) {
-                    const float f = ex2(ml[k * 16 + nt * 8 + r] - mm);
-                    const float4 v = *reinterpret_cast<const float4*>(mo + (size_t)(k * L::kMr + r) * L::kPitch + ch);
-                    ll = fmaf(f, ml[(kNdWarps + k) * 16 + nt * 8 + r], ll);
-                    acc.x = fmaf(f, v.x, acc.x);
-                    acc.y = fmaf(f, v.y, acc.y);
-                    acc.z = fmaf(f, v.z, acc.z);
-                    acc.w = fmaf(f, v.w, acc.w);
-                }
-                const int rr = nt * 8 + r;
+            merge(nt, [&](int r, int ch, float m_, float l_, float4 o_) {
                 if (whole) {
-                    nib_put<FP16>(G, A, row0, w.h, rr, D, ch, mm, ll, acc);
+                    nib_put<FP16>(G, A, row0, w.h, r, D, ch, m_, l_, o_);
                 } else {
-                    if (ch == 0) { rec[rr] = mm; rec[R + rr] = ll; }
-                    *reinterpret_cast<float4*>(rec + 2 * R + (size_t)rr * D + ch) = acc;
+                    if (ch == 0) { rec[r] = m_; rec[R + r] = l_; }
+                    *reinterpret_cast<float4*>(rec + 2 * R + (size_t)r * D + ch) = o_;
                 }
-            }
+            });
         }
         if (!whole) {                                    // the last CTA of this (request, kv-head) merges the records
             named_barrier(1, kNdThreads);
             if (tid == 0) {                              // the barrier, then one fence: the whole CTA's record is out
                 __threadfence();
-                const int c0 = cta_of(first), c1 = cta_of(first + w.units - 1);
+                const int c0 = cta_of(first), c1 = cta_of(first + w.real() - 1);
                 const int k = atomicAdd(A.tickets + c0, 1);
                 s_last[0] = k == c1 - c0;
                 s_last[1] = c0;
@@ -664,96 +678,84 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
             }
             named_barrier(1, kNdThreads);
             if (s_last[0]) {
-                // Each record's share of each row first (its maximum against the common one, in shared
-                // memory, kShares records at a time), then groups of rows D / 4 threads take every
-                // groups-th record, four channels of a row a thread; the groups' sums meet at the end.
-                constexpr int kRec = R * (D + 2), kShares = 64;
+                // A warp takes every kNdWarps-th record, a lane four channels of each row; the warps'
+                // sums then meet as those of the segment did.
+                constexpr int kRec = R * (D + 2), kLanes = D / 4;
                 const int c0 = s_last[1], c1 = s_last[2];
                 const int slot0 = first == each * c0 + extra * c0 / ctas ? 0 : 1;   // the first CTA's record; the others' are at 0
-                const float* recs = A.records + (size_t)(2 * c0 + slot0) * kRec;
-                auto record = [&](int c) { return c == c0 ? recs : A.records + (size_t)(2 * c) * kRec; };
-                float* sh = reinterpret_cast<float*>(sm + L::kMerge);           // [kShares][R] shares
-                float* top = reinterpret_cast<float*>(sm + L::kMl);             // [R] maximum, [R] sum
-                const int items = rows * (D / 4), groups = max(1, kNdThreads / items);
-                const int grp = items < kNdThreads ? tid / items : 0;
-                float4 acc[kTurns];
+                const int ch = lane % kLanes * 4, half = lane / kLanes;             // d 64: the half warps take a record each
+                constexpr int kHalves = 32 / kLanes;
 #pragma unroll
-                for (int k = 0; k < kTurns; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (tid < R) {
-                    top[tid] = kNdNone;
-                    top[R + tid] = 0.f;
-                }
-                named_barrier(1, kNdThreads);
-                for (int cb = c0; cb <= c1; cb += kShares) {
-                    const int nc = min(kShares, c1 - cb + 1);
-                    // a warp a row: the maximum over the records so far, shares against it
-                    for (int r = warp; r < rows; r += kNdWarps) {
-                        const bool a1 = lane < nc, a2 = lane + 32 < nc;
-                        const float* x1 = record(cb + (a1 ? lane : 0));
-                        const float* x2 = record(cb + (a2 ? lane + 32 : 0));
-                        const float m1 = a1 ? __ldcg(x1 + r) : kNdNone, m2 = a2 ? __ldcg(x2 + r) : kNdNone;
-                        const float l1 = a1 ? __ldcg(x1 + R + r) : 0.f, l2 = a2 ? __ldcg(x2 + R + r) : 0.f;
-                        float mm = fmaxf(m1, m2);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (nt) named_barrier(1, kNdThreads);
+                    float mm[L::kMr], ll[L::kMr];
+                    float4 acc[L::kMr];
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-                        const float was = top[r];
-                        mm = fmaxf(mm, was);
-                        const float f1 = a1 ? ex2(m1 - mm) : 0.f, f2 = a2 ? ex2(m2 - mm) : 0.f;
-                        float ll = f1 * l1 + f2 * l2;
+                    for (int r = 0; r < L::kMr; ++r) {
+                        mm[r] = kNdNone;
+                        ll[r] = 0.f;
+                        acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    constexpr int kAhead = L::kMr <= 4 ? 3 : 1;                     // records in flight
+                    for (int c = c0 + warp * kHalves + half; c - half <= c1; c += kNdWarps * kHalves * kAhead) {
+                        float m1[kAhead][L::kMr], l1[kAhead][L::kMr];
+                        float4 v[kAhead][L::kMr];
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(~0u, ll, o);
-                        sh[lane * R + r] = f1;
-                        sh[(lane + 32) * R + r] = f2;
-                        __syncwarp();
+                        for (int k = 0; k < kAhead; ++k) {
+                            const int ck = c + k * kNdWarps * kHalves;
+                            const float* x = A.records + (size_t)(2 * ck + (ck == c0 ? slot0 : 0)) * kRec + 8 * nt;
+#pragma unroll
+                            for (int r = 0; r < L::kMr; ++r) {
+                                const bool in = ck <= c1 && 8 * nt + r < rows;
+                                m1[k][r] = in ? __ldcg(x + r) : kNdNone;
+                                l1[k][r] = in ? __ldcg(x + R + r) : 0.f;
+                                v[k][r] = in ? __ldcg(reinterpret_cast<const float4*>(x - 8 * nt + 2 * R + (size_t)(8 * nt + r) * D + ch))
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                            for (int r = 0; r < L::kMr; ++r) {
+                                const float mn = fmaxf(mm[r], m1[k][r]), f0 = ex2(mm[r] - mn), f1 = ex2(m1[k][r] - mn);
+                                mm[r] = mn;
+                                ll[r] = fmaf(f1, l1[k][r], ll[r] * f0);
+                                acc[r].x = fmaf(f1, v[k][r].x, acc[r].x * f0);
+                                acc[r].y = fmaf(f1, v[k][r].y, acc[r].y * f0);
+                                acc[r].z = fmaf(f1, v[k][r].z, acc[r].z * f0);
+                                acc[r].w = fmaf(f1, v[k][r].w, acc[r].w * f0);
+                            }
+                    }
+                    if (kHalves == 2) {                  // the half warps' sums join
+#pragma unroll
+                        for (int r = 0; r < L::kMr; ++r) {
+                            const float mo_ = __shfl_xor_sync(~0u, mm[r], 16), mn = fmaxf(mm[r], mo_);
+                            const float f0 = ex2(mm[r] - mn);
+                            mm[r] = mn;
+                            ll[r] *= f0;
+                            acc[r].x *= f0; acc[r].y *= f0; acc[r].z *= f0; acc[r].w *= f0;
+                            ll[r] += __shfl_xor_sync(~0u, ll[r], 16);
+                            acc[r].x += __shfl_xor_sync(~0u, acc[r].x, 16);
+                            acc[r].y += __shfl_xor_sync(~0u, acc[r].y, 16);
+                            acc[r].z += __shfl_xor_sync(~0u, acc[r].z, 16);
+                            acc[r].w += __shfl_xor_sync(~0u, acc[r].w, 16);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < L::kMr; ++r) {
+                        if (half == 0) *reinterpret_cast<float4*>(mo + (size_t)(warp * L::kMr + r) * L::kPitch + ch) = acc[r];
                         if (lane == 0) {
-                            const float f0 = ex2(was - mm);
-                            top[r] = mm;
-                            top[R + r] = fmaf(top[R + r], f0, ll);
-                            sh[kShares * R + r] = f0;    // what was summed before
+                            ml[warp * 16 + nt * 8 + r] = mm[r];
+                            ml[(kNdWarps + warp) * 16 + nt * 8 + r] = ll[r];
                         }
                     }
                     named_barrier(1, kNdThreads);
-#pragma unroll
-                    for (int k = 0; k < kTurns; ++k) {
-                        const int e = (items < kNdThreads ? tid % items : tid) + k * kNdThreads;
-                        if (e >= items || grp >= groups) continue;
-                        const int r = e / (D / 4), ch = e % (D / 4) * 4;
-                        const float f0 = sh[kShares * R + r];
-                        acc[k].x *= f0; acc[k].y *= f0; acc[k].z *= f0; acc[k].w *= f0;
-#pragma unroll 8
-                        for (int c = grp; c < nc; c += groups) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(record(cb + c) + 2 * R + (size_t)r * D + ch));
-                            const float f = sh[c * R + r];
-                            acc[k].x = fmaf(f, v.x, acc[k].x);
-                            acc[k].y = fmaf(f, v.y, acc[k].y);
-                            acc[k].z = fmaf(f, v.z, acc[k].z);
-                            acc[k].w = fmaf(f, v.w, acc[k].w);
-                        }
-                    }
-                    named_barrier(1, kNdThreads);        // the shares are read
-                }
-                if (groups > 1) {                        // items < threads: one turn
-                    float4* part = reinterpret_cast<float4*>(sm + L::kMerge);
-                    part[tid] = acc[0];
-                    named_barrier(1, kNdThreads);
-                    if (tid < items)
-                        for (int k = 1; k < groups; ++k) {
-                            const float4 v = part[tid + k * items];
-                            acc[0].x += v.x; acc[0].y += v.y; acc[0].z += v.z; acc[0].w += v.w;
-                        }
-                }
-#pragma unroll
-                for (int k = 0; k < kTurns; ++k) {
-                    const int e = tid + k * kNdThreads;
-                    if (e < items) {
-                        const int r = e / (D / 4), ch = e % (D / 4) * 4;
-                        nib_put<FP16>(G, A, row0, w.h, r, D, ch, top[r], top[R + r], acc[k]);
-                    }
+                    merge(nt, [&](int r, int c, float m_, float l_, float4 o_) { nib_put<FP16>(G, A, row0, w.h, r, D, c, m_, l_, o_); });
                 }
             }
         }
         named_barrier(1, kNdThreads);                    // the merge rows are free for the next segment
-        at += cnt;
+        at += min(w.left, w.units - w.unit);
     }
 }
 

@@ -19,7 +19,7 @@ SOURCES = ["dwkv_api.cu", "dwkv_basis.cu", "dwkv_cache.cu", "dwkv_control.cu", "
            "dwkv_decode_b8.cu", "dwkv_decode_b8p.cu", "dwkv_decode_b4c8.cu", "dwkv_decode_b4pc8.cu",
            "dwkv_decode_b8c8.cu", "dwkv_decode_b8pc8.cu", "dwkv_nibble_api.cu", "dwkv_nibble_store.cu",
            "dwkv_nibble_attend.cu"]
-HEADERS = ["dwkv_common.cuh", "dwkv_decode.cuh", "dwkv_encode.cuh", "dwkv_stored.cuh", "dwkv_nibble.cuh", "dwkv_nibble_decode.cuh"]
+HEADERS = ["dwkv_common.cuh", "dwkv_decode.cuh", "dwkv_encode.cuh", "dwkv_stored.cuh", "dwkv_nibble.cuh", "dwkv_nibble_decode.cuh", "dwkv_nibble_chunk.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

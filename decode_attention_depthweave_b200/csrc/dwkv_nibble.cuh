@@ -93,7 +93,7 @@ struct NibAttend {
     const uint8_t* pool;
     uint16_t* out;                               // [n_rows][hq][d]
     float* lse;                                  // nullable [n_rows][hq]
-    int rows_hi;                                 // requests with more rows x heads than this are not this launch's
+    int rows_lo, rows_hi;                        // a launch takes requests of rows_lo < rows x heads <= rows_hi
     int* tickets;                                // [CTAs] zero between launches
     float* records;                              // [2 CTAs] parts of requests cut between CTAs
 };

@@ -265,7 +265,7 @@ dwkv_status dwkv_nibble_attention(dwkv_nibble_handle h, int32_t n_seqs, int32_t 
     if ((st = check_pool(pool)) != DWKV_OK) return st;
     NIB_DEVICE(h);
     const NibAttend A{n_seqs, n_rows, std::min(max_q, n_rows), q_stride, static_cast<const uint16_t*>(q), cu_rows, seq_lens,
-                      block_tables, static_cast<const uint8_t*>(pool), static_cast<uint16_t*>(out), lse, 0, nullptr, nullptr};
+                      block_tables, static_cast<const uint8_t*>(pool), static_cast<uint16_t*>(out), lse, 0, 0, nullptr, nullptr};
     const cudaError_t e = nib_attend(G, A, h->num_sms, h->arena, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "dwkv_nibble_attention launch");
     return DWKV_OK;

@@ -1,0 +1,668 @@
+// dwkv_nibble_chunk.cuh -- attention over the 4-bit cache for many rows a request (prompt chunks):
+// above kNdRows rows (query rows x query heads of a kv-head), on the 5th-generation tensor cores.
+//
+// Bound by the tensor cores and the exponentials alike: a (256 rows x 128 tokens) unit at d = 128 is
+// 2048 cycles of tcgen05.mma and 2048 of MUFU.  A CTA is one unit pipeline:
+//   loader      1 warp   bulk copies of 16-token blocks, 64 tokens a stage
+//   unpack      4 warps  codes -> fp16 keys and values (exact), written as swizzled operand tiles
+//   MMA         1 thread S = Q K^T (both from shared memory), O += P V (P from tensor memory)
+//   softmax     2 x 4 warps, a thread a row: maximum, exponentials, sum; P back to tensor memory over S
+// Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while
+// one is in its softmax, the other's products run.  Tensor memory: S0 S1 O0 O1, all 512 columns at d = 128.
+// The maximum may lag 2^8 behind (P carries 2^7, as in the decode kernel): O is rescaled only when
+// a row's maximum moves by more, and a tile is read from tensor memory once.
+//
+// K and V tiles have one layout, [token][64 channels] rows of 128 bytes, 16-byte chunks xored with
+// token % 8: the K-major swizzled layout for K (tokens are N, channels K) and the MN-major one for V
+// (channels are N, tokens K).  A word of codes unpacks to channels 0 4 1 5 2 6 3 7 of its eight: the
+// queries are stored in that order too, and the outputs are read back from it.
+//
+// Units of 128 tokens of a (request, kv-head, 256 rows), in flat order, are cut into equal ranges,
+// one a CTA, as in the decode kernel; cut items leave records that their last CTA merges.
+#pragma once
+#include "dwkv_nibble_decode.cuh"
+
+namespace dwkv {
+
+constexpr int kNcRows = 128;                             // of a tile
+constexpr int kNcTokens = 128;                           // of a unit
+constexpr int kNcBorder = 3;                             // what an item's end costs, in units (queries, epilogue)
+constexpr int kNcSoftmax = 256;                          // threads
+constexpr int kNcUnpackWarps = 4;
+constexpr int kNcThreads = kNcSoftmax + 32 * kNcUnpackWarps + 64;
+constexpr int kNcRawTokens = 64;                         // of a raw stage
+constexpr int kNcRawStages = 3;
+
+template <int D>
+struct NcLayout {
+    static constexpr uint32_t kTile = (uint32_t)kNcTokens * D * 2;                 // a fp16 tile of 128 rows
+    static constexpr uint32_t kHalf = (uint32_t)kNcTokens * 128;                   // its 64 channels
+    static constexpr uint32_t kBlock = 18u * D;
+    static constexpr uint32_t kRawStage = kNcRawTokens / kNibBlock * kBlock;
+    static constexpr uint32_t kQ = 0;                                              // [2] tiles
+    static constexpr uint32_t kK = 2 * kTile;                                      // [2] stages
+    static constexpr uint32_t kV = 4 * kTile;                                      // [2]
+    static constexpr uint32_t kRaw = 6 * kTile;                                    // [kNcRawStages]
+    static constexpr uint32_t kBars = kRaw + kNcRawStages * kRawStage;
+    static constexpr uint32_t kBytes = kBars + 512 + 1024;                         // barriers and words; slack to align the tiles
+    static constexpr int kRec = 2 * kNcRows * (D + 2);                             // floats of a record
+};
+
+// Items of a request: its tokens, rows and 256-row items.
+struct NcSpan {
+    int len, nq, items;
+    long long units;                                     // of one kv-head
+};
+// Item x of a request: first token and units.
+__device__ __forceinline__ void nc_item(const NibGeom& G, int len, int nq, int x, int& base, int& units) {
+    const int rows = nq * G.g, r0 = 2 * kNcRows * x, r1 = min(rows, r0 + 2 * kNcRows);
+    const int hi = len - nq + (r1 - 1) / G.g;
+    base = G.window > 0 ? max(0, len - nq + r0 / G.g - G.window + 1) & ~15 : 0;
+    units = max(1, (hi + 1 - base + kNcTokens - 1) / kNcTokens) + kNcBorder;
+}
+__device__ __forceinline__ NcSpan nc_span(const NibGeom& G, const NibAttend& A, int b) {
+    NcSpan s{0, 0, 0, 0};
+    if (!nib_request(G, A, b, s.len, s.nq) || s.nq == 0 || s.nq * G.g <= A.rows_lo) { s.nq = 0; return s; }
+    s.items = (s.nq * G.g + 2 * kNcRows - 1) / (2 * kNcRows);
+    for (int x = 0; x < s.items; ++x) {
+        int base, units;
+        nc_item(G, s.len, s.nq, x, base, units);
+        s.units += units;
+    }
+    return s;
+}
+
+// The walk over the segments (parts of items) of a CTA's range.
+struct NcWalk {
+    int b, h, x, unit;
+    long long left;
+    NcSpan s;
+    int base, units;                                     // of the item
+    __device__ __forceinline__ int real() const { return units - kNcBorder; }
+    __device__ __forceinline__ int count() const { return (int)min(left, (long long)(real() - unit)); }
+    __device__ __forceinline__ int step() const { return (int)min(left, (long long)(units - unit)); }
+    __device__ __forceinline__ bool next(const NibGeom& G, const NibAttend& A) {
+        left -= step();
+        if (left <= 0) return false;
+        unit = 0;
+        if (++x == s.items) {
+            x = 0;
+            if (++h == G.hkv) {
+                h = 0;
+                do {
+                    if (++b >= A.n) { left = 0; return false; }
+                    s = nc_span(G, A, b);
+                } while (s.items == 0);
+            }
+        }
+        nc_item(G, s.len, s.nq, x, base, units);
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint64_t nc_desc(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr >> 4) & 0x3fffu) | ((uint64_t)((lbo >> 4) & 0x3fffu) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void nc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void nc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void nc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void nc_ld32(uint32_t addr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void nc_st32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom G, const NibAttend A) {
+    using L = NcLayout<D>;
+    constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kNcTokens >> 3) << 17) | ((uint32_t)(kNcRows >> 4) << 24);
+    constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kNcRows >> 4) << 24);
+    constexpr uint32_t kTmS = 0, kTmO = 256;             // columns: S tiles at 0 and 128, O tiles behind
+    extern __shared__ uint8_t raw_sm[];
+    __shared__ int s_last[3];
+    __shared__ long long s_sum[16];
+    __shared__ int s_start[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t sbase = (smem_addr(raw_sm) + 1023u) & ~1023u;
+    uint8_t* sm = raw_sm + (sbase - smem_addr(raw_sm));
+    // barriers
+    const uint32_t bars = sbase + L::kBars;
+    auto raw_full = [&](int s) { return bars + 8u * s; };
+    auto raw_empty = [&](int s) { return bars + 32u + 8u * s; };
+    auto k_full = [&](int s) { return bars + 64u + 8u * s; };
+    auto k_empty = [&](int s) { return bars + 80u + 8u * s; };
+    auto v_full = [&](int s) { return bars + 96u + 8u * s; };
+    auto v_empty = [&](int s) { return bars + 112u + 8u * s; };
+    auto s_full = [&](int t) { return bars + 128u + 8u * t; };
+    auto p_ready = [&](int t) { return bars + 144u + 8u * t; };
+    const uint32_t o_full = bars + 160u, q_ready = bars + 168u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 176);
+    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 180);
+    uint8_t* raw_flags = sm + L::kBars + 192;            // [kNcRawStages] a bit a block that is not there
+    uint8_t* k_flags = sm + L::kBars + 200;              // [4] units: a bit a block that is not there
+    // Bounded wait; once one ran out, every role winds down.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 63u) == 0u && (*dead || global_ns() - t0 > kWaitLimitNs)) {
+                if (!*dead) nib_error(G, 6u /*DWKV_DEV_TIMEOUT*/, 0x6e63u, bar - bars);
+                *dead = 1;
+                return false;
+            }
+        }
+    };
+    if (tid == 0) {
+        for (int s = 0; s < kNcRawStages; ++s) {
+            mbar_init(raw_full(s), kNcRawTokens / kNibBlock);
+            mbar_init(raw_empty(s), kNcUnpackWarps);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(k_full(s), kNcUnpackWarps);
+            mbar_init(k_empty(s), 1u);
+            mbar_init(v_full(s), kNcUnpackWarps);
+            mbar_init(v_empty(s), 1u);
+            mbar_init(s_full(s), 1u);
+            mbar_init(p_ready(s), kNcRows);
+        }
+        mbar_init(o_full, 1u);
+        mbar_init(q_ready, kNcSoftmax);
+        *dead = 0;
+        fence_mbar_init();
+    }
+
+    // ---- this CTA's range of units: floor(total c / n) of them before CTA c
+    NcWalk w;
+    long long total, at;
+    int ctas;
+    {
+        const int per = (A.n + kNcThreads - 1) / kNcThreads;
+        const int b0 = min(A.n, tid * per), b1 = min(A.n, b0 + per);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += nc_span(G, A, b).units * G.hkv;
+        long long before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, before, o);
+            if (lane >= o) before += y;
+        }
+        if (lane == 31) s_sum[warp] = before;
+        before -= mine;
+        __syncthreads();
+        total = 0;
+        for (int k = 0; k < kNcThreads / 32; ++k) {
+            if (k == warp) before += total;
+            total += s_sum[k];
+        }
+        if (total == 0) return;
+        ctas = (int)min((long long)gridDim.x, total);
+        if ((int)blockIdx.x >= ctas) return;
+        at = total * blockIdx.x / ctas;
+        w.left = total * (blockIdx.x + 1) / ctas - at;
+        if (at >= before && at < before + mine) {
+            long long u = at - before;
+            for (int b = b0; b < b1; ++b) {
+                const NcSpan s = nc_span(G, A, b);
+                if (u < s.units * G.hkv) {
+                    s_start[0] = b;
+                    s_start[1] = (int)(u / s.units);
+                    u %= s.units;
+                    int x = 0, base, units;
+                    for (;; ++x) {
+                        nc_item(G, s.len, s.nq, x, base, units);
+                        if (u < units) break;
+                        u -= units;
+                    }
+                    s_start[2] = x;
+                    s_start[3] = (int)u;
+                    break;
+                }
+                u -= s.units * G.hkv;
+            }
+        }
+        __syncthreads();
+        w.b = s_start[0];
+        w.h = s_start[1];
+        w.x = s_start[2];
+        w.unit = s_start[3];
+        w.s = nc_span(G, A, w.b);
+        nc_item(G, w.s.len, w.s.nq, w.x, w.base, w.units);
+    }
+    const long long at0 = at;
+    if (w.unit >= w.real()) {                            // the range starts in the empty units behind an item
+        at += w.step();
+        if (!w.next(G, A)) return;
+    }
+    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == kNcSoftmax / 32 + kNcUnpackWarps + 1) {
+        // ================= loader: lane k copies block k of each raw stage
+        int stage = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (bool some = true; ok && some; some = w.next(G, A)) {
+            const int end = min(w.s.len, w.base + (w.unit + w.count()) * kNcTokens);
+            const int32_t* row = A.table + (size_t)w.b * G.max_blocks;
+            int t = w.base + w.unit * kNcTokens + 16 * lane;
+            const int stages = w.count() * (kNcTokens / kNcRawTokens);
+            const bool mine = lane < kNcRawTokens / kNibBlock;
+            int id = mine && t < end ? __ldg(row + (t >> G.page_shift)) : -1;
+            for (int u = 0; u < stages; ++u) {
+                const int tn = t + kNcRawTokens;
+                const int idn = mine && tn < end ? __ldg(row + (tn >> G.page_shift)) : -1;
+                if (round > 0 && !wait(raw_empty(stage), (round - 1) & 1u)) { ok = false; break; }
+                const bool there = mine && t < end, good = there && (unsigned)id < (unsigned)G.num_pages;
+                if (there && !good) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)w.b, (uint32_t)id);
+                const uint32_t have = __ballot_sync(~0u, good);
+                if (lane == 0) raw_flags[stage] = (uint8_t)(~have & ((1u << (kNcRawTokens / kNibBlock)) - 1u));
+                __syncwarp();
+                if (good) {
+                    mbar_arrive_expect_tx(raw_full(stage), L::kBlock);
+                    bulk_g2s(sbase + L::kRaw + stage * L::kRawStage + lane * L::kBlock,
+                             A.pool + nib_block_at(G, id, w.h, t & (G.page - 1)), L::kBlock, raw_full(stage));
+                } else if (mine) {
+                    mbar_arrive(raw_full(stage));
+                }
+                if (++stage == kNcRawStages) { stage = 0; ++round; }
+                t = tn;
+                id = idn;
+            }
+        }
+        if (!ok)                                         // the copies in flight end first, each wait with a limit
+            for (int s = 0; s < kNcRawStages; ++s)
+                if (round > 0 || s < stage) mbar_wait_for(raw_full(s), (round - (s >= stage)) & 1u, 10000000ull);
+    } else if (warp >= kNcSoftmax / 32 && warp < kNcSoftmax / 32 + kNcUnpackWarps) {
+        // ================= unpack: 64 tokens at a time, a warp a 16-token block; keys, then values
+        const int uw = warp - kNcSoftmax / 32;
+        const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
+        int stage = 0;
+        uint32_t round = 0;
+        uint32_t j = 0;                                  // units so far
+        bool ok = true;
+        for (bool some = true; ok && some; some = w.next(G, A)) {
+            const int cnt = w.count();
+            for (int u = 0; ok && u < cnt; ++u, ++j) {
+                const int buf = j & 1;
+                // the products that read this buffer two units ago are done: the scores', then the values'
+                if (j >= 2 && !wait(k_empty(buf), ((j >> 1) - 1) & 1u)) { ok = false; break; }
+                uint32_t lost = 0;
+#pragma unroll 1
+                for (int part = 0; part < kNcTokens / kNcRawTokens; ++part) {
+                    if (!wait(raw_full(stage), round & 1u)) { ok = false; break; }
+                    const uint32_t fl = raw_flags[stage];
+                    lost |= fl << (part * (kNcRawTokens / kNibBlock));
+                    const bool gone = (fl >> uw) & 1u;
+                    const uint8_t* blk = sm + L::kRaw + stage * L::kRawStage + uw * L::kBlock;
+                    const int row0 = part * kNcRawTokens + 16 * uw;      // the block's tokens in the tile
+                    const int left = w.s.len - (w.base + (w.unit + u) * kNcTokens + row0);   // tokens of the block that exist
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        if (z && part == 0 && j >= 2 && ok) ok = wait(v_empty(buf), ((j >> 1) - 1) & 1u);
+                        if (!ok) break;
+                        uint8_t* tile = sm + (z ? L::kV : L::kK) + buf * L::kTile;
+                        // eight lanes take one 32-channel chunk of eight tokens: loads of values and all stores
+                        // fall in distinct banks
+#pragma unroll
+                        for (int it = 0; it < D / 64; ++it) {
+                            const int q = it * 4 + (lane >> 3);              // (token half, chunk)
+                            const int t = (lane & 7) + 8 * (q & 1), c = q >> 1;
+                            uint4 cw = make_uint4(0, 0, 0, 0);
+                            uint32_t s0 = 0, s1 = 0;
+                            if (!gone && t < left) {                         // bytes behind the last token are not to be believed
+                                cw = *reinterpret_cast<const uint4*>(blk + (z ? nib_v_off(D, t, 16 * c) : nib_k_off(D, t) + 16 * c));
+                                s0 = blk[z ? nib_vscale_off(D, t, 2 * c) : nib_kscale_off(D, t, 2 * c)];
+                                s1 = blk[z ? nib_vscale_off(D, t, 2 * c + 1) : nib_kscale_off(D, t, 2 * c + 1)];
+                            }
+                            const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
+                            uint8_t* dst = tile + (c >> 1) * L::kHalf + (row0 + t) * 128;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t r = 0x00800080u * (y < 2 ? s0 : s1);
+                                uint32_t o[4];
+                                nib_unpack(words[y], r, hmul2_(r, kNibB0), hmul2_(r, kNibB1), e8, eh, o);
+                                *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + y) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+                        }
+                        if (z == 0 && part == kNcTokens / kNcRawTokens - 1) {
+                            if (uw == 0 && lane == 0) k_flags[j & 3u] = (uint8_t)lost;
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(k_full(buf));
+                        }
+                    }
+                    if (!ok) break;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_empty(stage));
+                    if (++stage == kNcRawStages) { stage = 0; ++round; }
+                }
+                if (!ok) break;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_full(buf));
+            }
+        }
+    } else if (warp == kNcSoftmax / 32 + kNcUnpackWarps) {
+        // ================= MMA: one thread
+        if (lane == 0) {
+            bool ok = true, any = false;
+            uint32_t j = 0, item = 0, pr[2] = {0, 0};
+            // O_t += P_t V of unit jj; first: O_t starts
+            auto pv = [&](int t, uint32_t jj, bool first) {
+                const int buf = jj & 1;
+                if (!wait(p_ready(t), pr[t] & 1u)) return false;
+                ++pr[t];
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t vb = sbase + L::kV + buf * L::kTile;
+#pragma unroll
+                for (int k = 0; k < kNcTokens / 16; ++k)
+                    nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + 8 * k, nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
+                              first && k == 0 ? 0u : 1u);
+                return true;
+            };
+            for (bool some = true; ok && some; some = w.next(G, A), ++item) {
+                const int cnt = w.count();
+                const int tiles = w.s.nq * G.g - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
+                ok = wait(q_ready, item & 1u);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int u = 0; ok && u <= cnt; ++u) {
+                    const int buf = j & 1;
+                    if (u < cnt) {
+                        ok = wait(k_full(buf), (j >> 1) & 1u);
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    }
+                    if (u > 0 && ok) ok = wait(v_full((j - 1) & 1), ((j - 1) >> 1) & 1u);
+                    for (int t = 0; ok && t < tiles; ++t) {
+                        if (u > 0 && !pv(t, j - 1, u == 1)) { ok = false; break; }
+                        if (u < cnt) {
+                            const uint32_t qb = sbase + L::kQ + t * L::kTile, kb = sbase + L::kK + buf * L::kTile;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * L::kHalf + (k & 3) * 32u;
+                                nc_mma_ss(tmem + kTmS + t * 128, nc_desc(qb + off, 16u), nc_desc(kb + off, 16u), kIdescS, k ? 1u : 0u);
+                            }
+                            nc_commit(s_full(t));
+                            any = true;
+                        }
+                    }
+                    if (!ok) break;
+                    if (u > 0) nc_commit(v_empty((j - 1) & 1));
+                    if (u < cnt) {
+                        nc_commit(k_empty(buf));
+                        ++j;
+                    } else {
+                        nc_commit(o_full);
+                    }
+                }
+            }
+            if (!ok && any) {                            // the products in flight end first, within a limit
+                nc_commit(o_full);
+                mbar_wait_for(o_full, item & 1u, 10000000ull);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================= softmax: a thread a row of tile t
+        const int t = warp >> 2, r = tid & (kNcRows - 1);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // this warp's tensor-memory lanes (32 of 128, bits 16 up)
+        const uint32_t s_at = tmem + lanes + kTmS + t * 128, o_at = tmem + lanes + kTmO + t * D;
+        uint32_t item = 0, sf = 0;
+        uint32_t j = 0;
+        bool ok = true;
+        for (bool some = true; ok && some; some = w.next(G, A), ++item) {
+            const int cnt = w.count(), rows = w.s.nq * G.g, row = 2 * kNcRows * w.x + kNcRows * t + r;
+            const int tiles = rows - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
+            const int row0 = A.cu[w.b];
+            const bool have = row < rows;
+            const int jq = have ? row / G.g : 0, hg = have ? row - jq * G.g : 0;
+            // ---- the query row, scaled by a power of two to below 2, as fp16
+            float fac = 1.f;
+            if (t < tiles) {
+                const uint16_t* qp = A.q + (size_t)(row0 + jq) * A.q_stride + (size_t)(w.h * G.g + hg) * D;
+                float a = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = have ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        a = fmaxf(a, fabsf(FP16 ? half_lo(x[y]) : bf16lo(x[y])));
+                        a = fmaxf(a, fabsf(FP16 ? half_hi(x[y]) : bf16hi(x[y])));
+                    }
+                }
+                const uint32_t e = min(max(__float_as_uint(a) >> 23, 1u), 253u);
+                const float sc = __uint_as_float((254u - e) << 23);
+                fac = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
+                uint8_t* dst = sm + L::kQ + t * L::kTile + r * 128;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = have ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    float f[8];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        f[2 * y] = (FP16 ? half_lo(x[y]) : bf16lo(x[y])) * sc;
+                        f[2 * y + 1] = (FP16 ? half_hi(x[y]) : bf16hi(x[y])) * sc;
+                    }
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kHalf + (((c & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
+                }
+                fence_async_smem();
+            }
+            mbar_arrive(q_ready);
+            const int hi = have ? w.s.len - w.s.nq + jq : -1;        // last token the row sees
+            // the tile's rows see all of a unit within [all_lo, all_hi]
+            const int tr0 = 2 * kNcRows * w.x + kNcRows * t, tr1 = min(rows, tr0 + kNcRows) - 1;
+            const int all_hi = w.s.len - w.s.nq + tr0 / G.g;
+            const int all_lo = G.window > 0 ? w.s.len - w.s.nq + max(tr1, 0) / G.g - G.window + 1 : 0;
+            float m = kNdNone, l = 0.f;
+            for (int u = 0; u < cnt; ++u, ++j) {
+                if (t >= tiles) continue;
+                if (!wait(s_full(t), sf & 1u)) { ok = false; break; }
+                ++sf;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const int t0 = w.base + (w.unit + u) * kNcTokens;
+                const uint32_t lost = k_flags[j & 3u];
+                const bool part = t0 + kNcTokens - 1 > all_hi || t0 < all_lo || lost;
+                uint32_t pk[kNcTokens / 2];
+                float sum, top;
+                for (bool again = false;;) {             // a second time when the maximum moves
+                    const float c0 = kNdBias - m;
+                    sum = 0.f;
+                    top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        nc_ld32(s_at + 32 * c, v);
+                        if (part) {
+                            asm volatile("" ::: "memory");
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) {
+                                const int tok = t0 + 32 * c + y;
+                                if (tok > hi || (G.window > 0 && tok <= hi - G.window) || ((lost >> (2 * c + (y >> 4))) & 1u)) v[y] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) top = fmaxf(top, v[y]);
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) {
+                            const float p0 = ex2(fmaf(v[y], fac, c0)), p1 = ex2(fmaf(v[y + 1], fac, c0));
+                            sum += p0 + p1;
+                            pk[16 * c + y / 2] = pack_half2(p0, p1);
+                        }
+                    }
+                    const float mx = top > -INFINITY ? top * fac : kNdNone;
+                    if (again || !__any_sync(~0u, mx > m + kNdLag)) break;
+                    again = true;
+                    const float mn = fmaxf(m, mx), f = ex2(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (u > 0) {                         // O holds the units before; its products are done
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float v[32];
+                            nc_ld32(o_at + 32 * c, v);
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) v[y] *= f;
+                            nc_st32(o_at + 32 * c, reinterpret_cast<const uint32_t*>(v));
+                        }
+                    }
+                }
+                l += sum;
+                nc_st32(s_at, pk);
+                nc_st32(s_at + 32, pk + 32);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                mbar_arrive(p_ready(t));
+            }
+            if (!ok) break;
+            // ---- the segment ends
+            if (!wait(o_full, item & 1u)) { ok = false; break; }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const bool whole = w.unit == 0 && cnt == w.real();
+            const long long first = at - w.unit;
+            const size_t out_at = (size_t)(row0 + jq) * G.hq + (size_t)(w.h * G.g + hg);
+            // eight channels from their stored order, normalised
+            auto put8 = [&](int c8, const float* v, float inv) {
+                uint32_t x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    // channel 2 y, 2 y + 1 of the eight: stored at 2 (c % 4) + c / 4
+                    const float a = v[(2 * y & 3) * 2 + (2 * y >> 2)] * inv, b = v[((2 * y + 1) & 3) * 2 + ((2 * y + 1) >> 2)] * inv;
+                    if (FP16) {
+                        x[y] = pack_half2(a, b);
+                    } else {
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
+                        x[y] = *reinterpret_cast<const uint32_t*>(&z);
+                    }
+                }
+                *reinterpret_cast<uint4*>(A.out + out_at * D + 8 * c8) = make_uint4(x[0], x[1], x[2], x[3]);
+            };
+            auto put_lse = [&](float m_, float l_) {
+                if (A.lse) A.lse[out_at] = l_ > 0.f ? (m_ - kNdBias + log2f(l_)) * 0.6931471805599453f : -INFINITY;
+            };
+            if (t < tiles) {
+                float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * L::kRec + (size_t)t * kNcRows * (D + 2);
+                const float inv = l > 0.f ? 32.f / l : 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    nc_ld32(o_at + 32 * c, v);
+                    if (whole) {
+                        if (have) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) put8(4 * c + y, v + 8 * y, inv);
+                        }
+                    } else {                             // [m][l][D / 4] of 128 rows each: rows side by side
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            *reinterpret_cast<float4*>(rec + 2 * kNcRows + (size_t)((8 * c + y) * kNcRows + r) * 4) =
+                                make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+                    }
+                }
+                if (whole) {
+                    if (have) put_lse(m, l);
+                } else {
+                    rec[r] = m;
+                    rec[kNcRows + r] = l;
+                }
+            }
+            if (!whole) {                                // the last CTA of this item merges the records
+                named_barrier(1, kNcSoftmax);
+                if (tid == 0) {
+                    __threadfence();
+                    const int c0 = cta_of(first), c1 = cta_of(first + w.real() - 1);
+                    const int k = atomicAdd(A.tickets + c0, 1);
+                    s_last[0] = k == c1 - c0;
+                    s_last[1] = c0;
+                    s_last[2] = c1;
+                    if (k == c1 - c0) A.tickets[c0] = 0;
+                    __threadfence();
+                }
+                named_barrier(1, kNcSoftmax);
+                if (s_last[0] && t < tiles && have) {
+                    const int c0 = s_last[1], c1 = s_last[2];
+                    const int slot0 = first == total * c0 / ctas ? 0 : 1;
+                    auto record = [&](int c) {
+                        return A.records + (size_t)(2 * c + (c == c0 ? slot0 : 0)) * L::kRec + (size_t)t * kNcRows * (D + 2);
+                    };
+                    float mm = kNdNone, ll = 0.f;
+                    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(record(c) + r));
+                    for (int c = c0; c <= c1; ++c) ll = fmaf(ex2(__ldcg(record(c) + r) - mm), __ldcg(record(c) + kNcRows + r), ll);
+                    const float inv = ll > 0.f ? 32.f / ll : 0.f;
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        float v[16];
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) v[y] = 0.f;
+#pragma unroll 2
+                        for (int c = c0; c <= c1; ++c) {
+                            const float* x = record(c);
+                            const float f = ex2(__ldcg(x + r) - mm);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const float4 z = __ldcg(reinterpret_cast<const float4*>(x + 2 * kNcRows + (size_t)((4 * q + y) * kNcRows + r) * 4));
+                                v[4 * y] = fmaf(f, z.x, v[4 * y]);
+                                v[4 * y + 1] = fmaf(f, z.y, v[4 * y + 1]);
+                                v[4 * y + 2] = fmaf(f, z.z, v[4 * y + 2]);
+                                v[4 * y + 3] = fmaf(f, z.w, v[4 * y + 3]);
+                            }
+                        }
+                        put8(2 * q, v, inv);
+                        put8(2 * q + 1, v + 8, inv);
+                    }
+                    put_lse(mm, ll);
+                }
+                named_barrier(1, kNcSoftmax);            // s_last is read
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            at += w.step();
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+}  // namespace dwkv

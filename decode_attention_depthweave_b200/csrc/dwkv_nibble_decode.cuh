@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                     qs[(nt * kWords + x) * 32] = make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]),
                                                             pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
             }
-            const float mult = G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23);
+            // not 0, however small the scale: a masked score is -inf times it
+            const float mult = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
             fac[nt][0] = __shfl_sync(~0u, mult, 8 * i);
             fac[nt][1] = __shfl_sync(~0u, mult, 8 * i + 4);
 #pragma unroll

@@ -3,10 +3,13 @@
 //
 // Bound by the tensor cores and the exponentials alike: a (256 rows x 128 tokens) unit at d = 128 is
 // 2048 cycles of tcgen05.mma and 2048 of MUFU.  A CTA is one unit pipeline:
-//   loader      1 warp   bulk copies of 16-token blocks, 64 tokens a stage
-//   unpack      4 warps  codes -> fp16 keys and values (exact), written as swizzled operand tiles
-//   MMA         1 thread S = Q K^T (both from shared memory), O += P V (P from tensor memory)
-//   softmax     2 x 4 warps, a thread a row: maximum, exponentials, sum; P back to tensor memory over S
+//   unpack      4 warps: each copies its 16-token blocks (a ring of bulk copies of its own) and turns
+//               their codes into fp16 keys and values (exact), written as swizzled operand tiles
+//   softmax     2 x 4 warps, a thread a row: maximum, exponentials, sum; P back to tensor memory over S.
+//               One thread of four warps issues their tile's products, S = Q K^T (from shared memory) and
+//               O += P V (P from tensor memory)
+// Twelve warps leave a thread 168 registers: a softmax thread holds 64 weights and up to 64 scores (with 14
+// warps and 128 registers it spilled: 8 us a unit).
 // Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while
 // one is in its softmax, the other's products run.  Tensor memory: S0 S1 O0 O1, all 512 columns at d = 128.
 // The maximum may lag 2^8 behind (P carries 2^7, as in the decode kernel): O is rescaled only when
@@ -29,21 +32,20 @@ constexpr int kNcTokens = 128;                           // of a unit
 constexpr int kNcBorder = 3;                             // what an item's end costs, in units (queries, epilogue)
 constexpr int kNcSoftmax = 256;                          // threads
 constexpr int kNcUnpackWarps = 4;
-constexpr int kNcThreads = kNcSoftmax + 32 * kNcUnpackWarps + 64;
-constexpr int kNcRawTokens = 64;                         // of a raw stage
-constexpr int kNcRawStages = 3;
+constexpr int kNcThreads = kNcSoftmax + 32 * kNcUnpackWarps;
+constexpr int kNcRawStages = 3;                          // blocks in flight a warp
+constexpr int kNcParts = kNcTokens / (kNibBlock * kNcUnpackWarps);      // blocks of a unit a warp
 
 template <int D>
 struct NcLayout {
     static constexpr uint32_t kTile = (uint32_t)kNcTokens * D * 2;                 // a fp16 tile of 128 rows
     static constexpr uint32_t kHalf = (uint32_t)kNcTokens * 128;                   // its 64 channels
     static constexpr uint32_t kBlock = 18u * D;
-    static constexpr uint32_t kRawStage = kNcRawTokens / kNibBlock * kBlock;
     static constexpr uint32_t kQ = 0;                                              // [2] tiles
     static constexpr uint32_t kK = 2 * kTile;                                      // [2] stages
     static constexpr uint32_t kV = 4 * kTile;                                      // [2]
-    static constexpr uint32_t kRaw = 6 * kTile;                                    // [kNcRawStages]
-    static constexpr uint32_t kBars = kRaw + kNcRawStages * kRawStage;
+    static constexpr uint32_t kRaw = 6 * kTile;                                    // [warps][kNcRawStages] blocks
+    static constexpr uint32_t kBars = kRaw + kNcUnpackWarps * kNcRawStages * kBlock;
     static constexpr uint32_t kBytes = kBars + 512 + 1024;                         // barriers and words; slack to align the tiles
     static constexpr int kRec = 2 * kNcRows * (D + 2);                             // floats of a record
 };
@@ -119,7 +121,8 @@ __device__ __forceinline__ void nc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 __device__ __forceinline__ void nc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void nc_ld32(uint32_t addr, float (&v)[32]) {
+// 32 columns of this lane's row; the values are there after nc_ld_wait().
+__device__ __forceinline__ void nc_ld32_issue(uint32_t addr, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -128,7 +131,36 @@ __device__ __forceinline__ void nc_ld32(uint32_t addr, float (&v)[32]) {
           "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
           "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Ties the values to the wait, so that no use moves before it.
+__device__ __forceinline__ void nc_ld_wait(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14])
+                 :: "memory");
+    asm volatile(""
+                 : "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                   "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
+                   "+f"(v[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void nc_ld32(uint32_t addr, float (&v)[32]) {
+    nc_ld32_issue(addr, v);
+    nc_ld_wait(v);
+}
+// a * b + c and a + b on two floats at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
 __device__ __forceinline__ void nc_st32(uint32_t addr, const uint32_t* v) {
     asm volatile(
@@ -149,7 +181,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kNcRows >> 4) << 24);
     constexpr uint32_t kTmS = 0, kTmO = 256;             // columns: S tiles at 0 and 128, O tiles behind
     extern __shared__ uint8_t raw_sm[];
-    __shared__ int s_last[3];
+    __shared__ int s_last[2][3];
     __shared__ long long s_sum[16];
     __shared__ int s_start[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -157,19 +189,16 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     uint8_t* sm = raw_sm + (sbase - smem_addr(raw_sm));
     // barriers
     const uint32_t bars = sbase + L::kBars;
-    auto raw_full = [&](int s) { return bars + 8u * s; };
-    auto raw_empty = [&](int s) { return bars + 32u + 8u * s; };
-    auto k_full = [&](int s) { return bars + 64u + 8u * s; };
-    auto k_empty = [&](int s) { return bars + 80u + 8u * s; };
-    auto v_full = [&](int s) { return bars + 96u + 8u * s; };
-    auto v_empty = [&](int s) { return bars + 112u + 8u * s; };
-    auto s_full = [&](int t) { return bars + 128u + 8u * t; };
-    auto p_ready = [&](int t) { return bars + 144u + 8u * t; };
-    const uint32_t o_full = bars + 160u, q_ready = bars + 168u;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 176);
-    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 180);
-    uint8_t* raw_flags = sm + L::kBars + 192;            // [kNcRawStages] a bit a block that is not there
-    uint8_t* k_flags = sm + L::kBars + 200;              // [4] units: a bit a block that is not there
+    auto k_full = [&](int s) { return bars + 8u * s; };
+    auto k_empty = [&](int s) { return bars + 16u + 8u * s; };
+    auto v_full = [&](int s) { return bars + 32u + 8u * s; };
+    auto v_empty = [&](int s) { return bars + 48u + 8u * s; };
+    auto s_full = [&](int t) { return bars + 64u + 8u * t; };
+    auto o_full = [&](int t) { return bars + 80u + 8u * t; };
+    auto raw_full = [&](int w, int s) { return bars + 96u + 8u * (w * kNcRawStages + s); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 256);
+    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 260);
+    uint8_t* k_flags = sm + L::kBars + 272;              // [4] units: [warps] a bit a block of the unit that is not there
     // Bounded wait; once one ran out, every role winds down.
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -184,20 +213,15 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
         }
     };
     if (tid == 0) {
-        for (int s = 0; s < kNcRawStages; ++s) {
-            mbar_init(raw_full(s), kNcRawTokens / kNibBlock);
-            mbar_init(raw_empty(s), kNcUnpackWarps);
-        }
         for (int s = 0; s < 2; ++s) {
             mbar_init(k_full(s), kNcUnpackWarps);
-            mbar_init(k_empty(s), 1u);
+            mbar_init(k_empty(s), 2u);                   // one for each tile
             mbar_init(v_full(s), kNcUnpackWarps);
-            mbar_init(v_empty(s), 1u);
+            mbar_init(v_empty(s), 2u);
             mbar_init(s_full(s), 1u);
-            mbar_init(p_ready(s), kNcRows);
+            mbar_init(o_full(s), 1u);
         }
-        mbar_init(o_full, 1u);
-        mbar_init(q_ready, kNcSoftmax);
+        for (int s = 0; s < kNcUnpackWarps * kNcRawStages; ++s) mbar_init(raw_full(0, s), 1u);
         *dead = 0;
         fence_mbar_init();
     }
@@ -274,69 +298,71 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == kNcSoftmax / 32 + kNcUnpackWarps + 1) {
-        // ================= loader: lane k copies block k of each raw stage
-        int stage = 0;
-        uint32_t round = 0;
-        bool ok = true;
-        for (bool some = true; ok && some; some = w.next(G, A)) {
-            const int end = min(w.s.len, w.base + (w.unit + w.count()) * kNcTokens);
-            const int32_t* row = A.table + (size_t)w.b * G.max_blocks;
-            int t = w.base + w.unit * kNcTokens + 16 * lane;
-            const int stages = w.count() * (kNcTokens / kNcRawTokens);
-            const bool mine = lane < kNcRawTokens / kNibBlock;
-            int id = mine && t < end ? __ldg(row + (t >> G.page_shift)) : -1;
-            for (int u = 0; u < stages; ++u) {
-                const int tn = t + kNcRawTokens;
-                const int idn = mine && tn < end ? __ldg(row + (tn >> G.page_shift)) : -1;
-                if (round > 0 && !wait(raw_empty(stage), (round - 1) & 1u)) { ok = false; break; }
-                const bool there = mine && t < end, good = there && (unsigned)id < (unsigned)G.num_pages;
-                if (there && !good) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)w.b, (uint32_t)id);
-                const uint32_t have = __ballot_sync(~0u, good);
-                if (lane == 0) raw_flags[stage] = (uint8_t)(~have & ((1u << (kNcRawTokens / kNibBlock)) - 1u));
-                __syncwarp();
-                if (good) {
-                    mbar_arrive_expect_tx(raw_full(stage), L::kBlock);
-                    bulk_g2s(sbase + L::kRaw + stage * L::kRawStage + lane * L::kBlock,
-                             A.pool + nib_block_at(G, id, w.h, t & (G.page - 1)), L::kBlock, raw_full(stage));
-                } else if (mine) {
-                    mbar_arrive(raw_full(stage));
-                }
-                if (++stage == kNcRawStages) { stage = 0; ++round; }
-                t = tn;
-                id = idn;
-            }
-        }
-        if (!ok)                                         // the copies in flight end first, each wait with a limit
-            for (int s = 0; s < kNcRawStages; ++s)
-                if (round > 0 || s < stage) mbar_wait_for(raw_full(s), (round - (s >= stage)) & 1u, 10000000ull);
-    } else if (warp >= kNcSoftmax / 32 && warp < kNcSoftmax / 32 + kNcUnpackWarps) {
-        // ================= unpack: 64 tokens at a time, a warp a 16-token block; keys, then values
+    if (warp >= kNcSoftmax / 32) {
+        // ================= unpack: blocks uw and uw + 4 of each unit; keys, then values
         const int uw = warp - kNcSoftmax / 32;
         const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
+        // the copies' side: the block p_t of the walk p, in page p_id
+        NcWalk p = w;
+        bool p_more = true;
+        int p_left, p_t, p_end, p_id = -1, p_stage = 0;
+        uint32_t holes = 0;                              // stages whose block is not there
+        auto p_open = [&]() {
+            p_left = p.count() * kNcParts;
+            p_t = p.base + p.unit * kNcTokens + kNibBlock * uw;
+            p_end = min(p.s.len, p.base + (p.unit + p.count()) * kNcTokens);
+        };
+        auto p_look = [&]() {
+            if (p_more && p_t < p_end) p_id = __ldg(A.table + (size_t)p.b * G.max_blocks + (p_t >> G.page_shift));
+        };
+        auto p_issue = [&]() {
+            if (!p_more) return;
+            const bool there = p_t < p_end, good = there && (unsigned)p_id < (unsigned)G.num_pages;
+            const uint32_t bar = raw_full(uw, p_stage);
+            holes = good ? holes & ~(1u << p_stage) : holes | 1u << p_stage;
+            if (lane == 0) {
+                if (good) {
+                    mbar_arrive_expect_tx(bar, L::kBlock);
+                    bulk_g2s(sbase + L::kRaw + (uint32_t)(uw * kNcRawStages + p_stage) * L::kBlock,
+                             A.pool + nib_block_at(G, p_id, p.h, p_t & (G.page - 1)), L::kBlock, bar);
+                } else {
+                    mbar_arrive(bar);
+                    if (there) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)p.b, (uint32_t)p_id);
+                }
+            }
+            p_stage = p_stage + 1 == kNcRawStages ? 0 : p_stage + 1;
+            p_t += kNibBlock * kNcUnpackWarps;
+            if (--p_left == 0) {
+                p_more = p.next(G, A);
+                if (p_more) p_open();
+            }
+            p_look();
+        };
+        p_open();
+        p_look();
+        for (int s = 0; s < kNcRawStages; ++s) p_issue();
         int stage = 0;
-        uint32_t round = 0;
-        uint32_t j = 0;                                  // units so far
+        uint32_t phase = 0, j = 0;                       // j: units so far
         bool ok = true;
         for (bool some = true; ok && some; some = w.next(G, A)) {
             const int cnt = w.count();
             for (int u = 0; ok && u < cnt; ++u, ++j) {
                 const int buf = j & 1;
+                const uint32_t before = ((j >> 1) - 1) & 1u;
                 // the products that read this buffer two units ago are done: the scores', then the values'
-                if (j >= 2 && !wait(k_empty(buf), ((j >> 1) - 1) & 1u)) { ok = false; break; }
+                if (j >= 2 && !wait(k_empty(buf), before)) { ok = false; break; }
                 uint32_t lost = 0;
 #pragma unroll 1
-                for (int part = 0; part < kNcTokens / kNcRawTokens; ++part) {
-                    if (!wait(raw_full(stage), round & 1u)) { ok = false; break; }
-                    const uint32_t fl = raw_flags[stage];
-                    lost |= fl << (part * (kNcRawTokens / kNibBlock));
-                    const bool gone = (fl >> uw) & 1u;
-                    const uint8_t* blk = sm + L::kRaw + stage * L::kRawStage + uw * L::kBlock;
-                    const int row0 = part * kNcRawTokens + 16 * uw;      // the block's tokens in the tile
+                for (int part = 0; part < kNcParts; ++part) {
+                    if (!wait(raw_full(uw, stage), phase)) { ok = false; break; }
+                    const bool gone = (holes >> stage) & 1u;
+                    lost |= (uint32_t)gone << part;
+                    const uint8_t* blk = sm + L::kRaw + (uw * kNcRawStages + stage) * L::kBlock;
+                    const int row0 = kNibBlock * (part * kNcUnpackWarps + uw);                // the block's tokens in the tile
                     const int left = w.s.len - (w.base + (w.unit + u) * kNcTokens + row0);   // tokens of the block that exist
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        if (z && part == 0 && j >= 2 && ok) ok = wait(v_empty(buf), ((j >> 1) - 1) & 1u);
+                        if (z && part == 0 && j >= 2) ok = wait(v_empty(buf), before);
                         if (!ok) break;
                         uint8_t* tile = sm + (z ? L::kV : L::kK) + buf * L::kTile;
                         // eight lanes take one 32-channel chunk of eight tokens: loads of values and all stores
@@ -362,17 +388,20 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                                 *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + y) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                             }
                         }
-                        if (z == 0 && part == kNcTokens / kNcRawTokens - 1) {
-                            if (uw == 0 && lane == 0) k_flags[j & 3u] = (uint8_t)lost;
+                        if (z == 0 && part == kNcParts - 1) {
+                            if (lane == 0) k_flags[(j & 3u) * kNcUnpackWarps + uw] = (uint8_t)lost;
                             fence_async_smem();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(k_full(buf));
                         }
                     }
                     if (!ok) break;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(raw_empty(stage));
-                    if (++stage == kNcRawStages) { stage = 0; ++round; }
+                    __syncwarp();                        // the block is read: its stage takes another
+                    p_issue();
+                    if (++stage == kNcRawStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
                 if (!ok) break;
                 fence_async_smem();
@@ -380,82 +409,67 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 if (lane == 0) mbar_arrive(v_full(buf));
             }
         }
-    } else if (warp == kNcSoftmax / 32 + kNcUnpackWarps) {
-        // ================= MMA: one thread
-        if (lane == 0) {
-            bool ok = true, any = false;
-            uint32_t j = 0, item = 0, pr[2] = {0, 0};
-            // O_t += P_t V of unit jj; first: O_t starts
-            auto pv = [&](int t, uint32_t jj, bool first) {
-                const int buf = jj & 1;
-                if (!wait(p_ready(t), pr[t] & 1u)) return false;
-                ++pr[t];
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t vb = sbase + L::kV + buf * L::kTile;
-#pragma unroll
-                for (int k = 0; k < kNcTokens / 16; ++k)
-                    nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + 8 * k, nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
-                              first && k == 0 ? 0u : 1u);
-                return true;
-            };
-            for (bool some = true; ok && some; some = w.next(G, A), ++item) {
-                const int cnt = w.count();
-                const int tiles = w.s.nq * G.g - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
-                ok = wait(q_ready, item & 1u);
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int u = 0; ok && u <= cnt; ++u) {
-                    const int buf = j & 1;
-                    if (u < cnt) {
-                        ok = wait(k_full(buf), (j >> 1) & 1u);
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    }
-                    if (u > 0 && ok) ok = wait(v_full((j - 1) & 1), ((j - 1) >> 1) & 1u);
-                    for (int t = 0; ok && t < tiles; ++t) {
-                        if (u > 0 && !pv(t, j - 1, u == 1)) { ok = false; break; }
-                        if (u < cnt) {
-                            const uint32_t qb = sbase + L::kQ + t * L::kTile, kb = sbase + L::kK + buf * L::kTile;
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = (k >> 2) * L::kHalf + (k & 3) * 32u;
-                                nc_mma_ss(tmem + kTmS + t * 128, nc_desc(qb + off, 16u), nc_desc(kb + off, 16u), kIdescS, k ? 1u : 0u);
-                            }
-                            nc_commit(s_full(t));
-                            any = true;
-                        }
-                    }
-                    if (!ok) break;
-                    if (u > 0) nc_commit(v_empty((j - 1) & 1));
-                    if (u < cnt) {
-                        nc_commit(k_empty(buf));
-                        ++j;
-                    } else {
-                        nc_commit(o_full);
-                    }
-                }
-            }
-            if (!ok && any) {                            // the products in flight end first, within a limit
-                nc_commit(o_full);
-                mbar_wait_for(o_full, item & 1u, 10000000ull);
-            }
-        }
-        __syncwarp();
+        if (!ok)                                         // the copies in flight end first, each wait with a limit
+            for (int k = 0; k < kNcRawStages; ++k)
+                mbar_wait_for(raw_full(uw, (stage + k) % kNcRawStages), phase ^ (uint32_t)(stage + k >= kNcRawStages), 10000000ull);
     } else {
         // ================= softmax: a thread a row of tile t
+        // A wait that ran out leaves ok false: the loops run to their end without waiting or issuing, so
+        // that every thread meets the others at the barriers.
         const int t = warp >> 2, r = tid & (kNcRows - 1);
+        const bool issuer = r == 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // this warp's tensor-memory lanes (32 of 128, bits 16 up)
         const uint32_t s_at = tmem + lanes + kTmS + t * 128, o_at = tmem + lanes + kTmO + t * D;
-        uint32_t item = 0, sf = 0;
-        uint32_t j = 0;
+        uint32_t items = 0, j = 0, units = 0;            // segments and units of this tile; units of the CTA
         bool ok = true;
-        for (bool some = true; ok && some; some = w.next(G, A), ++item) {
+        // S of unit jj; O += P V of unit jj (first: O starts)
+        auto issue_qk = [&](uint32_t jj) {
+            const int buf = jj & 1;
+            if (ok) ok = wait(k_full(buf), (jj >> 1) & 1u);
+            if (!ok) return;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t qb = sbase + L::kQ + t * L::kTile, kb = sbase + L::kK + buf * L::kTile;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * L::kHalf + (k & 3) * 32u;
+                nc_mma_ss(tmem + kTmS + t * 128, nc_desc(qb + off, 16u), nc_desc(kb + off, 16u), kIdescS, k ? 1u : 0u);
+            }
+            nc_commit(s_full(t));
+            nc_commit(k_empty(buf));
+        };
+        auto issue_pv = [&](uint32_t jj, bool first) {
+            const int buf = jj & 1;
+            if (ok) ok = wait(v_full(buf), (jj >> 1) & 1u);
+            if (!ok) return;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t vb = sbase + L::kV + buf * L::kTile;
+#pragma unroll
+            for (int k = 0; k < kNcTokens / 16; ++k)
+                nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + 8 * k, nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
+                          first && k == 0 ? 0u : 1u);
+            nc_commit(v_empty(buf));
+        };
+        for (bool some = true; some; some = w.next(G, A)) {
             const int cnt = w.count(), rows = w.s.nq * G.g, row = 2 * kNcRows * w.x + kNcRows * t + r;
             const int tiles = rows - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
+            if (t >= tiles) {                            // no such tile: its consent to each unit's buffers
+                for (int u = 0; u < cnt; ++u, ++units)
+                    if (issuer && ok) {
+                        const int buf = units & 1;
+                        ok = wait(k_full(buf), (units >> 1) & 1u);
+                        if (ok) mbar_arrive(k_empty(buf));
+                        if (ok) ok = wait(v_full(buf), (units >> 1) & 1u);
+                        if (ok) mbar_arrive(v_empty(buf));
+                    }
+                at += w.step();
+                continue;
+            }
             const int row0 = A.cu[w.b];
             const bool have = row < rows;
             const int jq = have ? row / G.g : 0, hg = have ? row - jq * G.g : 0;
             // ---- the query row, scaled by a power of two to below 2, as fp16
             float fac = 1.f;
-            if (t < tiles) {
+            {
                 const uint16_t* qp = A.q + (size_t)(row0 + jq) * A.q_stride + (size_t)(w.h * G.g + hg) * D;
                 float a = 0.f;
 #pragma unroll 4
@@ -487,48 +501,68 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 }
                 fence_async_smem();
             }
-            mbar_arrive(q_ready);
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            named_barrier(1 + t, kNcRows);               // the tile's queries are there, its O is read
+            if (issuer) issue_qk(units);
             const int hi = have ? w.s.len - w.s.nq + jq : -1;        // last token the row sees
             // the tile's rows see all of a unit within [all_lo, all_hi]
             const int tr0 = 2 * kNcRows * w.x + kNcRows * t, tr1 = min(rows, tr0 + kNcRows) - 1;
             const int all_hi = w.s.len - w.s.nq + tr0 / G.g;
             const int all_lo = G.window > 0 ? w.s.len - w.s.nq + max(tr1, 0) / G.g - G.window + 1 : 0;
+            // a bit for each of the 32 tokens from t on: seen by this row and there (gone: a bit a block that is not)
+            auto seen_of = [&](int tok, uint32_t gone) {
+                const int n = hi - tok;                              // the last one seen
+                uint32_t bits = n >= 31 ? ~0u : n < 0 ? 0u : (2u << n) - 1u;
+                if (G.window > 0) {
+                    const int f = n - G.window + 1;                  // the first one seen
+                    bits &= f <= 0 ? ~0u : f > 31 ? 0u : ~0u << f;
+                }
+                return bits & ~((gone & 1u ? 0xffffu : 0u) | (gone & 2u ? 0xffff0000u : 0u));
+            };
             float m = kNdNone, l = 0.f;
-            for (int u = 0; u < cnt; ++u, ++j) {
-                if (t >= tiles) continue;
-                if (!wait(s_full(t), sf & 1u)) { ok = false; break; }
-                ++sf;
+            for (int u = 0; u < cnt; ++u, ++j, ++units) {
+                if (ok) ok = wait(s_full(t), j & 1u);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const int t0 = w.base + (w.unit + u) * kNcTokens;
-                const uint32_t lost = k_flags[j & 3u];
+                const uint32_t lost = *reinterpret_cast<const uint32_t*>(k_flags + (units & 3u) * kNcUnpackWarps);   // a byte a warp
                 const bool part = t0 + kNcTokens - 1 > all_hi || t0 < all_lo || lost;
                 uint32_t pk[kNcTokens / 2];
                 float sum, top;
                 for (bool again = false;;) {             // a second time when the maximum moves
-                    const float c0 = kNdBias - m;
-                    sum = 0.f;
-                    top = -INFINITY;
+                    const float2 c0 = make_float2(kNdBias - m, kNdBias - m), f2 = make_float2(fac, fac);
+                    float2 sums[4];
+                    float tops[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        nc_ld32(s_at + 32 * c, v);
+                    for (int y = 0; y < 4; ++y) {
+                        sums[y] = make_float2(0.f, 0.f);
+                        tops[y] = -INFINITY;
+                    }
+                    float v[2][32];
+                    nc_ld32_issue(s_at, v[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {        // the next columns come while these are worked on
+                        float (&x)[32] = v[c & 1];
+                        nc_ld_wait(x);
+                        if (c < 3) nc_ld32_issue(s_at + 32 * (c + 1), v[(c + 1) & 1]);
                         if (part) {
-                            asm volatile("" ::: "memory");
+                            // blocks 2 c and 2 c + 1 of the unit
+                            const uint32_t seen = seen_of(t0 + 32 * c, (lost >> (16 * (c & 1) + (c >> 1)) & 1u) |
+                                                                           (lost >> (16 * (c & 1) + 8 + (c >> 1)) & 1u) << 1);
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) {
-                                const int tok = t0 + 32 * c + y;
-                                if (tok > hi || (G.window > 0 && tok <= hi - G.window) || ((lost >> (2 * c + (y >> 4))) & 1u)) v[y] = -INFINITY;
-                            }
+                            for (int y = 0; y < 32; ++y) x[y] = (seen >> y) & 1u ? x[y] : -INFINITY;
                         }
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) top = fmaxf(top, v[y]);
 #pragma unroll
                         for (int y = 0; y < 32; y += 2) {
-                            const float p0 = ex2(fmaf(v[y], fac, c0)), p1 = ex2(fmaf(v[y + 1], fac, c0));
-                            sum += p0 + p1;
-                            pk[16 * c + y / 2] = pack_half2(p0, p1);
+                            tops[(y >> 1) & 3] = fmaxf(tops[(y >> 1) & 3], fmaxf(x[y], x[y + 1]));
+                            const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
+                            const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                            sums[(y >> 1) & 3] = add2(sums[(y >> 1) & 3], p);
+                            pk[16 * c + y / 2] = pack_half2(p.x, p.y);
                         }
                     }
+                    const float2 sa = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                    sum = sa.x + sa.y;
+                    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     const float mx = top > -INFINITY ? top * fac : kNdNone;
                     if (again || !__any_sync(~0u, mx > m + kNdLag)) break;
                     again = true;
@@ -551,11 +585,16 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 nc_st32(s_at + 32, pk + 32);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                mbar_arrive(p_ready(t));
+                named_barrier(1 + t, kNcRows);           // P is there
+                if (issuer) {
+                    issue_pv(units, u == 0);
+                    if (u + 1 < cnt) issue_qk(units + 1);
+                    else if (ok) nc_commit(o_full(t));
+                }
             }
-            if (!ok) break;
             // ---- the segment ends
-            if (!wait(o_full, item & 1u)) { ok = false; break; }
+            if (ok) ok = wait(o_full(t), items & 1u);
+            ++items;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const bool whole = w.unit == 0 && cnt == w.real();
             const long long first = at - w.unit;
@@ -579,7 +618,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             auto put_lse = [&](float m_, float l_) {
                 if (A.lse) A.lse[out_at] = l_ > 0.f ? (m_ - kNdBias + log2f(l_)) * 0.6931471805599453f : -INFINITY;
             };
-            if (t < tiles) {
+            {
                 float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * L::kRec + (size_t)t * kNcRows * (D + 2);
                 const float inv = l > 0.f ? 32.f / l : 0.f;
 #pragma unroll 1
@@ -606,20 +645,20 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 }
             }
             if (!whole) {                                // the last CTA of this item merges the records
-                named_barrier(1, kNcSoftmax);
-                if (tid == 0) {
+                named_barrier(1 + t, kNcRows);
+                if (issuer) {                            // the barrier, then one fence: the whole tile's record is out
                     __threadfence();
                     const int c0 = cta_of(first), c1 = cta_of(first + w.real() - 1);
-                    const int k = atomicAdd(A.tickets + c0, 1);
-                    s_last[0] = k == c1 - c0;
-                    s_last[1] = c0;
-                    s_last[2] = c1;
-                    if (k == c1 - c0) A.tickets[c0] = 0;
+                    const int k = atomicAdd(A.tickets + 2 * c0 + t, 1);
+                    s_last[t][0] = k == c1 - c0;
+                    s_last[t][1] = c0;
+                    s_last[t][2] = c1;
+                    if (k == c1 - c0) A.tickets[2 * c0 + t] = 0;
                     __threadfence();
                 }
-                named_barrier(1, kNcSoftmax);
-                if (s_last[0] && t < tiles && have) {
-                    const int c0 = s_last[1], c1 = s_last[2];
+                named_barrier(1 + t, kNcRows);
+                if (s_last[t][0] && have) {
+                    const int c0 = s_last[t][1], c1 = s_last[t][2];
                     const int slot0 = first == total * c0 / ctas ? 0 : 1;
                     auto record = [&](int c) {
                         return A.records + (size_t)(2 * c + (c == c0 ? slot0 : 0)) * L::kRec + (size_t)t * kNcRows * (D + 2);
@@ -651,10 +690,14 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     }
                     put_lse(mm, ll);
                 }
-                named_barrier(1, kNcSoftmax);            // s_last is read
+                named_barrier(1 + t, kNcRows);           // s_last is read
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             at += w.step();
+        }
+        if (!ok && issuer) {                             // the products in flight end first, within a limit
+            nc_commit(o_full(t));
+            mbar_wait_for(o_full(t), items & 1u, 10000000ull);
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

@@ -3,15 +3,17 @@
 //
 // Bound by the tensor cores and the exponentials alike: a (256 rows x 128 tokens) unit at d = 128 is
 // 2048 cycles of tcgen05.mma and 2048 of MUFU.  A CTA is one unit pipeline:
-//   unpack      4 warps: each copies its 16-token blocks (a ring of bulk copies of its own) and turns
+//   unpack      3 warps: each copies its 16-token blocks (a ring of bulk copies of its own) and turns
 //               their codes into fp16 keys and values (exact), written as swizzled operand tiles
-//   softmax     2 x 4 warps, a thread a row: maximum, exponentials, sum; P back to tensor memory over S.
-//               One thread of four warps issues their tile's products, S = Q K^T (from shared memory) and
-//               O += P V (P from tensor memory)
+//   MMA         1 thread: S = Q K^T (from shared memory), O += P V (P from tensor memory).  Issuing waits
+//               while the tensor cores are busy: done by a softmax thread, its warp waited too (1.38 ms)
+//   softmax     2 x 4 warps, a thread a row: maximum, exponentials, sum; P back to tensor memory over S
 // Twelve warps leave a thread 168 registers: a softmax thread holds 64 weights and up to 64 scores (with 14
 // warps and 128 registers it spilled: 8 us a unit).
-// Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while
-// one is in its softmax, the other's products run.  Tensor memory: S0 S1 O0 O1, all 512 columns at d = 128.
+// Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while one is in
+// its softmax, the other's products run.  (Scores in two pieces of 64 tokens, so that a tile's own products
+// run beside its softmax, were slower: with 64 columns a score product took 190 cycles, with 128 70.)
+// Tensor memory: S0 S1 O0 O1, all 512 columns at d = 128.
 // The maximum may lag 2^8 behind (P carries 2^7, as in the decode kernel): O is rescaled only when
 // a row's maximum moves by more, and a tile is read from tensor memory once.
 //
@@ -31,10 +33,10 @@ constexpr int kNcRows = 128;                             // of a tile
 constexpr int kNcTokens = 128;                           // of a unit
 constexpr int kNcBorder = 3;                             // what an item's end costs, in units (queries, epilogue)
 constexpr int kNcSoftmax = 256;                          // threads
-constexpr int kNcUnpackWarps = 4;
-constexpr int kNcThreads = kNcSoftmax + 32 * kNcUnpackWarps;
-constexpr int kNcRawStages = 3;                          // blocks in flight a warp
-constexpr int kNcParts = kNcTokens / (kNibBlock * kNcUnpackWarps);      // blocks of a unit a warp
+constexpr int kNcUnpackWarps = 3;
+constexpr int kNcThreads = kNcSoftmax + 32 * kNcUnpackWarps + 32;
+constexpr int kNcRawStages = 4;                          // blocks in flight a warp
+constexpr int kNcBlocks = kNcTokens / kNibBlock;         // of a unit
 
 template <int D>
 struct NcLayout {
@@ -194,11 +196,13 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     auto v_full = [&](int s) { return bars + 32u + 8u * s; };
     auto v_empty = [&](int s) { return bars + 48u + 8u * s; };
     auto s_full = [&](int t) { return bars + 64u + 8u * t; };
-    auto o_full = [&](int t) { return bars + 80u + 8u * t; };
-    auto raw_full = [&](int w, int s) { return bars + 96u + 8u * (w * kNcRawStages + s); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 256);
-    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 260);
-    uint8_t* k_flags = sm + L::kBars + 272;              // [4] units: [warps] a bit a block of the unit that is not there
+    auto p_ready = [&](int t) { return bars + 80u + 8u * t; };
+    auto raw_full = [&](int w, int s) { return bars + 128u + 8u * (w * kNcRawStages + s); };
+    auto o_full = [&](int t) { return bars + 248u + 8u * t; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 296);
+    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 300);
+    const uint32_t q_ready = bars + 240u;
+    uint8_t* k_flags = sm + L::kBars + 304;              // [4] units: [4] a bit a block of the unit that is not there, a byte a warp
     // Bounded wait; once one ran out, every role winds down.
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -215,13 +219,16 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(k_full(s), kNcUnpackWarps);
-            mbar_init(k_empty(s), 2u);                   // one for each tile
+            mbar_init(k_empty(s), 1u);
             mbar_init(v_full(s), kNcUnpackWarps);
-            mbar_init(v_empty(s), 2u);
+            mbar_init(v_empty(s), 1u);
             mbar_init(s_full(s), 1u);
+            mbar_init(p_ready(s), kNcRows);
             mbar_init(o_full(s), 1u);
         }
         for (int s = 0; s < kNcUnpackWarps * kNcRawStages; ++s) mbar_init(raw_full(0, s), 1u);
+        mbar_init(q_ready, kNcSoftmax);
+        for (int s = 0; s < 4; ++s) reinterpret_cast<uint32_t*>(k_flags)[s] = 0;
         *dead = 0;
         fence_mbar_init();
     }
@@ -298,104 +305,128 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= kNcSoftmax / 32) {
-        // ================= unpack: blocks uw and uw + 4 of each unit; keys, then values
+    if (warp >= kNcSoftmax / 32 && warp < kNcSoftmax / 32 + kNcUnpackWarps) {
+        // ================= unpack: every third block, from block (uw + j) % 3 of unit j on; keys, then values
         const int uw = warp - kNcSoftmax / 32;
         const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
         // the copies' side: the block p_t of the walk p, in page p_id
         NcWalk p = w;
         bool p_more = true;
-        int p_left, p_t, p_end, p_id = -1, p_stage = 0;
+        int p_j = 0, p_blk, p_units, p_t0, p_end, p_id = -1, p_stage = 0;
         uint32_t holes = 0;                              // stages whose block is not there
         auto p_open = [&]() {
-            p_left = p.count() * kNcParts;
-            p_t = p.base + p.unit * kNcTokens + kNibBlock * uw;
-            p_end = min(p.s.len, p.base + (p.unit + p.count()) * kNcTokens);
+            p_units = p.count();
+            p_t0 = p.base + p.unit * kNcTokens;
+            p_end = min(p.s.len, p_t0 + p_units * kNcTokens);
         };
         auto p_look = [&]() {
-            if (p_more && p_t < p_end) p_id = __ldg(A.table + (size_t)p.b * G.max_blocks + (p_t >> G.page_shift));
+            const int t = p_t0 + kNibBlock * p_blk;
+            if (p_more && t < p_end) p_id = __ldg(A.table + (size_t)p.b * G.max_blocks + (t >> G.page_shift));
         };
         auto p_issue = [&]() {
             if (!p_more) return;
-            const bool there = p_t < p_end, good = there && (unsigned)p_id < (unsigned)G.num_pages;
+            const int t = p_t0 + kNibBlock * p_blk;
+            const bool there = t < p_end, good = there && (unsigned)p_id < (unsigned)G.num_pages;
             const uint32_t bar = raw_full(uw, p_stage);
             holes = good ? holes & ~(1u << p_stage) : holes | 1u << p_stage;
             if (lane == 0) {
                 if (good) {
                     mbar_arrive_expect_tx(bar, L::kBlock);
                     bulk_g2s(sbase + L::kRaw + (uint32_t)(uw * kNcRawStages + p_stage) * L::kBlock,
-                             A.pool + nib_block_at(G, p_id, p.h, p_t & (G.page - 1)), L::kBlock, bar);
+                             A.pool + nib_block_at(G, p_id, p.h, t & (G.page - 1)), L::kBlock, bar);
                 } else {
                     mbar_arrive(bar);
                     if (there) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)p.b, (uint32_t)p_id);
                 }
             }
             p_stage = p_stage + 1 == kNcRawStages ? 0 : p_stage + 1;
-            p_t += kNibBlock * kNcUnpackWarps;
-            if (--p_left == 0) {
-                p_more = p.next(G, A);
-                if (p_more) p_open();
+            p_blk += kNcUnpackWarps;
+            if (p_blk >= kNcBlocks) {
+                ++p_j;
+                p_blk = (uw + p_j) % kNcUnpackWarps;
+                p_t0 += kNcTokens;
+                if (--p_units == 0) {
+                    p_more = p.next(G, A);
+                    if (p_more) p_open();
+                }
             }
             p_look();
         };
+        p_blk = uw % kNcUnpackWarps;
         p_open();
         p_look();
         for (int s = 0; s < kNcRawStages; ++s) p_issue();
+        // One block's keys (z = 0) or values into rows row0 .. row0 + 15 of a tile; `left`: its tokens that
+        // exist (the bytes behind them are not to be believed).  Eight lanes take one 32-channel chunk of eight
+        // tokens: all stores, and the loads of values, fall in distinct banks.  All loads come before the
+        // first store, which the compiler could not know to be elsewhere.
+        auto unpack = [&](int z, const uint8_t* blk, uint8_t* tile, int row0, int left) {
+            constexpr int kIts = D / 64;
+            uint4 cw[kIts];
+            uint32_t s0[kIts], s1[kIts];
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int q = it * 4 + (lane >> 3), t = (lane & 7) + 8 * (q & 1), c = q >> 1;    // (token half, chunk)
+                cw[it] = make_uint4(0, 0, 0, 0);
+                s0[it] = s1[it] = 0;
+                if (t < left) {
+                    cw[it] = *reinterpret_cast<const uint4*>(blk + (z ? nib_v_off(D, t, 16 * c) : nib_k_off(D, t) + 16 * c));
+                    s0[it] = blk[z ? nib_vscale_off(D, t, 2 * c) : nib_kscale_off(D, t, 2 * c)];
+                    s1[it] = blk[z ? nib_vscale_off(D, t, 2 * c + 1) : nib_kscale_off(D, t, 2 * c + 1)];
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int q = it * 4 + (lane >> 3), t = (lane & 7) + 8 * (q & 1), c = q >> 1;
+                const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
+                const uint32_t r0 = 0x00800080u * s0[it], r1 = 0x00800080u * s1[it];
+                const uint32_t b00 = hmul2_(r0, kNibB0), b01 = hmul2_(r0, kNibB1), b10 = hmul2_(r1, kNibB0), b11 = hmul2_(r1, kNibB1);
+                uint8_t* dst = tile + (c >> 1) * L::kHalf + (row0 + t) * 128;
+                uint32_t o[4][4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) nib_unpack(words[y], y < 2 ? r0 : r1, y < 2 ? b00 : b10, y < 2 ? b01 : b11, e8, eh, o[y]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + y) ^ (t & 7)) << 4)) = make_uint4(o[y][0], o[y][1], o[y][2], o[y][3]);
+            }
+        };
         int stage = 0;
         uint32_t phase = 0, j = 0;                       // j: units so far
         bool ok = true;
         for (bool some = true; ok && some; some = w.next(G, A)) {
             const int cnt = w.count();
             for (int u = 0; ok && u < cnt; ++u, ++j) {
-                const int buf = j & 1;
+                const int buf = j & 1, first = (int)((uw + j) % kNcUnpackWarps);
+                const int end = w.s.len - (w.base + (w.unit + u) * kNcTokens);       // tokens that exist, from the unit's first on
                 const uint32_t before = ((j >> 1) - 1) & 1u;
-                // the products that read this buffer two units ago are done: the scores', then the values'
-                if (j >= 2 && !wait(k_empty(buf), before)) { ok = false; break; }
                 uint32_t lost = 0;
+                // the keys of the warp's blocks, then their values: the scores are waited for first.  A
+                // buffer is free when the products that read it two units ago are done
+                ok = j < 2 || wait(k_empty(buf), before);
+                int st = stage;
+                uint32_t ph = phase;
 #pragma unroll 1
-                for (int part = 0; part < kNcParts; ++part) {
-                    if (!wait(raw_full(uw, stage), phase)) { ok = false; break; }
-                    const bool gone = (holes >> stage) & 1u;
-                    lost |= (uint32_t)gone << part;
-                    const uint8_t* blk = sm + L::kRaw + (uw * kNcRawStages + stage) * L::kBlock;
-                    const int row0 = kNibBlock * (part * kNcUnpackWarps + uw);                // the block's tokens in the tile
-                    const int left = w.s.len - (w.base + (w.unit + u) * kNcTokens + row0);   // tokens of the block that exist
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        if (z && part == 0 && j >= 2) ok = wait(v_empty(buf), before);
-                        if (!ok) break;
-                        uint8_t* tile = sm + (z ? L::kV : L::kK) + buf * L::kTile;
-                        // eight lanes take one 32-channel chunk of eight tokens: loads of values and all stores
-                        // fall in distinct banks
-#pragma unroll
-                        for (int it = 0; it < D / 64; ++it) {
-                            const int q = it * 4 + (lane >> 3);              // (token half, chunk)
-                            const int t = (lane & 7) + 8 * (q & 1), c = q >> 1;
-                            uint4 cw = make_uint4(0, 0, 0, 0);
-                            uint32_t s0 = 0, s1 = 0;
-                            if (!gone && t < left) {                         // bytes behind the last token are not to be believed
-                                cw = *reinterpret_cast<const uint4*>(blk + (z ? nib_v_off(D, t, 16 * c) : nib_k_off(D, t) + 16 * c));
-                                s0 = blk[z ? nib_vscale_off(D, t, 2 * c) : nib_kscale_off(D, t, 2 * c)];
-                                s1 = blk[z ? nib_vscale_off(D, t, 2 * c + 1) : nib_kscale_off(D, t, 2 * c + 1)];
-                            }
-                            const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
-                            uint8_t* dst = tile + (c >> 1) * L::kHalf + (row0 + t) * 128;
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const uint32_t r = 0x00800080u * (y < 2 ? s0 : s1);
-                                uint32_t o[4];
-                                nib_unpack(words[y], r, hmul2_(r, kNibB0), hmul2_(r, kNibB1), e8, eh, o);
-                                *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + y) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
-                        }
-                        if (z == 0 && part == kNcParts - 1) {
-                            if (lane == 0) k_flags[(j & 3u) * kNcUnpackWarps + uw] = (uint8_t)lost;
-                            fence_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(k_full(buf));
-                        }
+                for (int x = first; ok && x < kNcBlocks; x += kNcUnpackWarps) {
+                    if (!wait(raw_full(uw, st), ph)) { ok = false; break; }
+                    const bool gone = (holes >> st) & 1u;
+                    lost |= (uint32_t)gone << x;
+                    unpack(0, sm + L::kRaw + (uw * kNcRawStages + st) * L::kBlock, sm + L::kK + buf * L::kTile, kNibBlock * x,
+                           gone ? 0 : end - kNibBlock * x);
+                    if (++st == kNcRawStages) {
+                        st = 0;
+                        ph ^= 1u;
                     }
-                    if (!ok) break;
+                }
+                if (!ok) break;
+                if (lane == 0) k_flags[(j & 3u) * 4 + uw] = (uint8_t)lost;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(k_full(buf));
+                if (j >= 2 && !wait(v_empty(buf), before)) { ok = false; break; }
+#pragma unroll 1
+                for (int x = first; x < kNcBlocks; x += kNcUnpackWarps) {
+                    unpack(1, sm + L::kRaw + (uw * kNcRawStages + stage) * L::kBlock, sm + L::kV + buf * L::kTile, kNibBlock * x,
+                           (lost >> x) & 1u ? 0 : end - kNibBlock * x);
                     __syncwarp();                        // the block is read: its stage takes another
                     p_issue();
                     if (++stage == kNcRawStages) {
@@ -403,7 +434,6 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                         phase ^= 1u;
                     }
                 }
-                if (!ok) break;
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_full(buf));
@@ -412,56 +442,84 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
         if (!ok)                                         // the copies in flight end first, each wait with a limit
             for (int k = 0; k < kNcRawStages; ++k)
                 mbar_wait_for(raw_full(uw, (stage + k) % kNcRawStages), phase ^ (uint32_t)(stage + k >= kNcRawStages), 10000000ull);
+    } else if (warp == kNcSoftmax / 32 + kNcUnpackWarps) {
+        // ================= MMA: one thread
+        if (lane == 0) {
+            bool ok = true, any = false;
+            uint32_t j = 0, items = 0, done[2] = {0, 0};  // units; segments; units of each tile
+            // S of unit jj; O += P V of it (start: O starts)
+            auto qk = [&](int t, uint32_t jj) {
+                const uint32_t qb = sbase + L::kQ + t * L::kTile, kb = sbase + L::kK + (jj & 1) * L::kTile;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * L::kHalf + (k & 3) * 32u;
+                    nc_mma_ss(tmem + kTmS + t * 128, nc_desc(qb + off, 16u), nc_desc(kb + off, 16u), kIdescS, k ? 1u : 0u);
+                }
+                nc_commit(s_full(t));
+                any = true;
+            };
+            auto pv = [&](int t, uint32_t jj, bool start) {
+                const uint32_t vb = sbase + L::kV + (jj & 1) * L::kTile;
+#pragma unroll
+                for (int k = 0; k < kNcTokens / 16; ++k)
+                    nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + 8 * k, nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
+                              start && k == 0 ? 0u : 1u);
+            };
+            auto after = [&](bool got) {
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                return got;
+            };
+            for (bool some = true; ok && some; some = w.next(G, A), ++items) {
+                const int cnt = w.count(), tiles = w.s.nq * G.g - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
+                ok = after(wait(q_ready, items & 1u) && wait(k_full(j & 1), (j >> 1) & 1u));
+                if (!ok) break;
+                for (int t = 0; t < tiles; ++t) qk(t, j);
+                nc_commit(k_empty(j & 1));
+                for (int u = 0; ok && u < cnt; ++u, ++j) {
+                    for (int t = 0; ok && t < tiles; ++t) {
+                        ok = wait(p_ready(t), done[t] & 1u);
+                        ++done[t];
+                        if (ok && t == 0) ok = wait(v_full(j & 1), (j >> 1) & 1u);
+                        if (!after(ok)) break;
+                        pv(t, j, u == 0);
+                        if (u + 1 == cnt) {
+                            nc_commit(o_full(t));
+                        } else {
+                            if (t == 0) ok = after(wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1u));
+                            if (ok) qk(t, j + 1);
+                        }
+                    }
+                    if (!ok) break;
+                    nc_commit(v_empty(j & 1));
+                    if (u + 1 < cnt) nc_commit(k_empty((j + 1) & 1));
+                }
+            }
+            if (!ok && any) {                            // the products in flight end first, within a limit
+                nc_commit(s_full(0));
+                mbar_wait_for(s_full(0), j & 1u, 10000000ull);
+            }
+        }
+        __syncwarp();
     } else {
         // ================= softmax: a thread a row of tile t
         // A wait that ran out leaves ok false: the loops run to their end without waiting or issuing, so
         // that every thread meets the others at the barriers.
         const int t = warp >> 2, r = tid & (kNcRows - 1);
-        const bool issuer = r == 0;
+        const bool leader = r == 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // this warp's tensor-memory lanes (32 of 128, bits 16 up)
         const uint32_t s_at = tmem + lanes + kTmS + t * 128, o_at = tmem + lanes + kTmO + t * D;
-        uint32_t items = 0, j = 0, units = 0;            // segments and units of this tile; units of the CTA
+        uint32_t j = 0, items = 0, units = 0, segs = 0;  // units and segments of this tile, of the CTA
         bool ok = true;
-        // S of unit jj; O += P V of unit jj (first: O starts)
-        auto issue_qk = [&](uint32_t jj) {
-            const int buf = jj & 1;
-            if (ok) ok = wait(k_full(buf), (jj >> 1) & 1u);
-            if (!ok) return;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t qb = sbase + L::kQ + t * L::kTile, kb = sbase + L::kK + buf * L::kTile;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * L::kHalf + (k & 3) * 32u;
-                nc_mma_ss(tmem + kTmS + t * 128, nc_desc(qb + off, 16u), nc_desc(kb + off, 16u), kIdescS, k ? 1u : 0u);
-            }
-            nc_commit(s_full(t));
-            nc_commit(k_empty(buf));
-        };
-        auto issue_pv = [&](uint32_t jj, bool first) {
-            const int buf = jj & 1;
-            if (ok) ok = wait(v_full(buf), (jj >> 1) & 1u);
-            if (!ok) return;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t vb = sbase + L::kV + buf * L::kTile;
-#pragma unroll
-            for (int k = 0; k < kNcTokens / 16; ++k)
-                nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + 8 * k, nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
-                          first && k == 0 ? 0u : 1u);
-            nc_commit(v_empty(buf));
-        };
         for (bool some = true; some; some = w.next(G, A)) {
             const int cnt = w.count(), rows = w.s.nq * G.g, row = 2 * kNcRows * w.x + kNcRows * t + r;
             const int tiles = rows - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
-            if (t >= tiles) {                            // no such tile: its consent to each unit's buffers
-                for (int u = 0; u < cnt; ++u, ++units)
-                    if (issuer && ok) {
-                        const int buf = units & 1;
-                        ok = wait(k_full(buf), (units >> 1) & 1u);
-                        if (ok) mbar_arrive(k_empty(buf));
-                        if (ok) ok = wait(v_full(buf), (units >> 1) & 1u);
-                        if (ok) mbar_arrive(v_empty(buf));
-                    }
+            if (t >= tiles) {                            // no such tile; the queries' barrier counts all the same
+                mbar_arrive(q_ready);
+                units += cnt;
                 at += w.step();
+                // the next arrival belongs to the next segment: not before this one has begun
+                if (ok) ok = wait(q_ready, segs & 1u);
+                ++segs;
                 continue;
             }
             const int row0 = A.cu[w.b];
@@ -502,8 +560,8 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 fence_async_smem();
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            named_barrier(1 + t, kNcRows);               // the tile's queries are there, its O is read
-            if (issuer) issue_qk(units);
+            mbar_arrive(q_ready);                        // the tile's queries are there, its O is read
+            ++segs;
             const int hi = have ? w.s.len - w.s.nq + jq : -1;        // last token the row sees
             // the tile's rows see all of a unit within [all_lo, all_hi]
             const int tr0 = 2 * kNcRows * w.x + kNcRows * t, tr1 = min(rows, tr0 + kNcRows) - 1;
@@ -524,8 +582,9 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 if (ok) ok = wait(s_full(t), j & 1u);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const int t0 = w.base + (w.unit + u) * kNcTokens;
-                const uint32_t lost = *reinterpret_cast<const uint32_t*>(k_flags + (units & 3u) * kNcUnpackWarps);   // a byte a warp
-                const bool part = t0 + kNcTokens - 1 > all_hi || t0 < all_lo || lost;
+                uint32_t lost = *reinterpret_cast<const uint32_t*>(k_flags + (units & 3u) * 4);
+                lost |= lost >> 8 | lost >> 16;          // a bit a block
+                const bool part = t0 + kNcTokens - 1 > all_hi || t0 < all_lo || (lost & 255u);
                 uint32_t pk[kNcTokens / 2];
                 float sum, top;
                 for (bool again = false;;) {             // a second time when the maximum moves
@@ -545,9 +604,8 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                         nc_ld_wait(x);
                         if (c < 3) nc_ld32_issue(s_at + 32 * (c + 1), v[(c + 1) & 1]);
                         if (part) {
-                            // blocks 2 c and 2 c + 1 of the unit
-                            const uint32_t seen = seen_of(t0 + 32 * c, (lost >> (16 * (c & 1) + (c >> 1)) & 1u) |
-                                                                           (lost >> (16 * (c & 1) + 8 + (c >> 1)) & 1u) << 1);
+                            asm volatile("" ::: "memory");
+                            const uint32_t seen = seen_of(t0 + 32 * c, lost >> (2 * c));
 #pragma unroll
                             for (int y = 0; y < 32; ++y) x[y] = (seen >> y) & 1u ? x[y] : -INFINITY;
                         }
@@ -569,14 +627,15 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     const float mn = fmaxf(m, mx), f = ex2(m - mn);
                     m = mn;
                     l *= f;
-                    if (u > 0) {                         // O holds the units before; its products are done
+                    if (u > 0) {                         // O holds the units before: these scores came after their products
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
-                            float v[32];
-                            nc_ld32(o_at + 32 * c, v);
+                            float o[32];
+                            nc_ld32(o_at + 32 * c, o);
+                            uint32_t ou[32];
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) v[y] *= f;
-                            nc_st32(o_at + 32 * c, reinterpret_cast<const uint32_t*>(v));
+                            for (int y = 0; y < 32; ++y) ou[y] = __float_as_uint(o[y] * f);
+                            nc_st32(o_at + 32 * c, ou);
                         }
                     }
                 }
@@ -585,12 +644,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 nc_st32(s_at + 32, pk + 32);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                named_barrier(1 + t, kNcRows);           // P is there
-                if (issuer) {
-                    issue_pv(units, u == 0);
-                    if (u + 1 < cnt) issue_qk(units + 1);
-                    else if (ok) nc_commit(o_full(t));
-                }
+                mbar_arrive(p_ready(t));
             }
             // ---- the segment ends
             if (ok) ok = wait(o_full(t), items & 1u);
@@ -646,7 +700,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             }
             if (!whole) {                                // the last CTA of this item merges the records
                 named_barrier(1 + t, kNcRows);
-                if (issuer) {                            // the barrier, then one fence: the whole tile's record is out
+                if (leader) {                            // the barrier, then one fence: the whole tile's record is out
                     __threadfence();
                     const int c0 = cta_of(first), c1 = cta_of(first + w.real() - 1);
                     const int k = atomicAdd(A.tickets + 2 * c0 + t, 1);
@@ -694,10 +748,6 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             at += w.step();
-        }
-        if (!ok && issuer) {                             // the products in flight end first, within a limit
-            nc_commit(o_full(t));
-            mbar_wait_for(o_full(t), items & 1u, 10000000ull);
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

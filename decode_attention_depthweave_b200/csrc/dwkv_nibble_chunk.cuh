@@ -2,20 +2,23 @@
 // above kNdRows rows (query rows x query heads of a kv-head), on the 5th-generation tensor cores.
 //
 // Bound by the tensor cores and the exponentials alike: a (256 rows x 128 tokens) unit at d = 128 is
-// 2048 cycles of tcgen05.mma and 2048 of MUFU.  A CTA is one unit pipeline:
-//   unpack      3 warps: each copies its 16-token blocks (a ring of bulk copies of its own) and turns
-//               their codes into fp16 keys and values (exact), written as swizzled operand tiles
+// 2048 cycles of tcgen05.mma and 2048 of MUFU.  A CTA's warps:
+//   loader      1 warp: bulk copies of the keys' and the values' half of each 16-token block
 //   MMA         1 thread: S = Q K^T (from shared memory), O += P V (P from tensor memory).  Issuing waits
-//               while the tensor cores are busy: done by a softmax thread, its warp waited too (1.38 ms)
-//   softmax     2 x 4 warps, a thread a row: maximum, exponentials, sum; P back to tensor memory over S
-// Twelve warps leave a thread 168 registers: a softmax thread holds 64 weights and up to 64 scores (with 14
-// warps and 128 registers it spilled: 8 us a unit).
+//               while the tensor cores are busy: done by a softmax thread, its warp waited too
+//   softmax     2 tiles x 8 warps, two threads a row (64 tokens each): maximum, exponentials, sum; P back to
+//               tensor memory over S.  While their products run, the warps turn the next units' codes into fp16
+//               keys (tile 0's warps, two units ahead) and values (tile 1's, one ahead: the furthest that two
+//               buffers of each allow), exact, written as swizzled operand tiles: half a block a warp
+// With a thread a row (eight warps) a unit took 5800 cycles: two warps a scheduler, each in its own chain
+// of latencies; warps of their own for the unpacking made it no shorter (1.37 ms).
+//
 // Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while one is in
 // its softmax, the other's products run.  (Scores in two pieces of 64 tokens, so that a tile's own products
 // run beside its softmax, were slower: with 64 columns a score product took 190 cycles, with 128 70.)
 // Tensor memory: S0 S1 O0 O1, all 512 columns at d = 128.
 // The maximum may lag 2^8 behind (P carries 2^7, as in the decode kernel): O is rescaled only when
-// a row's maximum moves by more, and a tile is read from tensor memory once.
+// a row's maximum moves by more.
 //
 // K and V tiles have one layout, [token][64 channels] rows of 128 bytes, 16-byte chunks xored with
 // token % 8: the K-major swizzled layout for K (tokens are N, channels K) and the MN-major one for V
@@ -25,6 +28,8 @@
 // Units of 128 tokens of a (request, kv-head, 256 rows), in flat order, are cut into equal ranges,
 // one a CTA, as in the decode kernel; cut items leave records that their last CTA merges.
 #pragma once
+#include <type_traits>
+
 #include "dwkv_nibble_decode.cuh"
 
 namespace dwkv {
@@ -32,11 +37,11 @@ namespace dwkv {
 constexpr int kNcRows = 128;                             // of a tile
 constexpr int kNcTokens = 128;                           // of a unit
 constexpr int kNcBorder = 3;                             // what an item's end costs, in units (queries, epilogue)
-constexpr int kNcSoftmax = 256;                          // threads
-constexpr int kNcUnpackWarps = 3;
-constexpr int kNcThreads = kNcSoftmax + 32 * kNcUnpackWarps + 32;
-constexpr int kNcRawStages = 4;                          // blocks in flight a warp
-constexpr int kNcBlocks = kNcTokens / kNibBlock;         // of a unit
+constexpr int kNcSoftmax = 512;                          // threads
+constexpr int kNcTile = 256;                             // of a tile
+constexpr int kNcThreads = kNcSoftmax + 64;
+constexpr int kNcBlocks = kNcTokens / kNibBlock;         // of a unit: its keys or values one a warp of a tile
+static_assert(kNcBlocks * 32 == kNcTile, "a block a warp");
 
 template <int D>
 struct NcLayout {
@@ -46,9 +51,10 @@ struct NcLayout {
     static constexpr uint32_t kQ = 0;                                              // [2] tiles
     static constexpr uint32_t kK = 2 * kTile;                                      // [2] stages
     static constexpr uint32_t kV = 4 * kTile;                                      // [2]
-    static constexpr uint32_t kRaw = 6 * kTile;                                    // [warps][kNcRawStages] blocks
-    static constexpr uint32_t kBars = kRaw + kNcUnpackWarps * kNcRawStages * kBlock;
-    static constexpr uint32_t kBytes = kBars + 512 + 1024;                         // barriers and words; slack to align the tiles
+    static constexpr uint32_t kRaw = 6 * kTile;                                    // keys' half blocks, values'
+    static constexpr uint32_t kBars = kRaw + kNcBlocks * kBlock;
+    static constexpr uint32_t kEx = kBars + 512;                                   // [2][2 tiles][2][128] maxima, sums
+    static constexpr uint32_t kBytes = kEx + 4096 + 1024;                         // barriers and words; slack to align the tiles
     static constexpr int kRec = 2 * kNcRows * (D + 2);                             // floats of a record
 };
 
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     constexpr uint32_t kTmS = 0, kTmO = 256;             // columns: S tiles at 0 and 128, O tiles behind
     extern __shared__ uint8_t raw_sm[];
     __shared__ int s_last[2][3];
-    __shared__ long long s_sum[16];
+    __shared__ long long s_sum[kNcThreads / 32];
     __shared__ int s_start[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t sbase = (smem_addr(raw_sm) + 1023u) & ~1023u;
@@ -197,12 +203,14 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     auto v_empty = [&](int s) { return bars + 48u + 8u * s; };
     auto s_full = [&](int t) { return bars + 64u + 8u * t; };
     auto p_ready = [&](int t) { return bars + 80u + 8u * t; };
-    auto raw_full = [&](int w, int s) { return bars + 128u + 8u * (w * kNcRawStages + s); };
-    auto o_full = [&](int t) { return bars + 248u + 8u * t; };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 296);
-    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 300);
-    const uint32_t q_ready = bars + 240u;
-    uint8_t* k_flags = sm + L::kBars + 304;              // [4] units: [4] a bit a block of the unit that is not there, a byte a warp
+    auto o_full = [&](int t) { return bars + 96u + 8u * t; };
+    auto raw_full = [&](int z) { return bars + 112u + 8u * z; };     // 0 keys, 1 values
+    auto raw_empty = [&](int z) { return bars + 128u + 8u * z; };
+    const uint32_t q_ready = bars + 144u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBars + 152);
+    volatile int* dead = reinterpret_cast<volatile int*>(sm + L::kBars + 156);
+    uint8_t* raw_left = sm + L::kBars + 160;             // [2][blocks] tokens of a raw block that exist
+    uint8_t* lost_at = sm + L::kBars + 176;              // [8] units: [blocks] 1: not there
     // Bounded wait; once one ran out, every role winds down.
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -218,17 +226,17 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     };
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(k_full(s), kNcUnpackWarps);
+            mbar_init(k_full(s), kNcBlocks);
             mbar_init(k_empty(s), 1u);
-            mbar_init(v_full(s), kNcUnpackWarps);
+            mbar_init(v_full(s), kNcBlocks);
             mbar_init(v_empty(s), 1u);
             mbar_init(s_full(s), 1u);
-            mbar_init(p_ready(s), kNcRows);
+            mbar_init(p_ready(s), kNcTile);
             mbar_init(o_full(s), 1u);
+            mbar_init(raw_full(s), kNcBlocks);
+            mbar_init(raw_empty(s), kNcBlocks);
         }
-        for (int s = 0; s < kNcUnpackWarps * kNcRawStages; ++s) mbar_init(raw_full(0, s), 1u);
         mbar_init(q_ready, kNcSoftmax);
-        for (int s = 0; s < 4; ++s) reinterpret_cast<uint32_t*>(k_flags)[s] = 0;
         *dead = 0;
         fence_mbar_init();
     }
@@ -305,144 +313,53 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= kNcSoftmax / 32 && warp < kNcSoftmax / 32 + kNcUnpackWarps) {
-        // ================= unpack: every third block, from block (uw + j) % 3 of unit j on; keys, then values
-        const int uw = warp - kNcSoftmax / 32;
-        const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
-        // the copies' side: the block p_t of the walk p, in page p_id
-        NcWalk p = w;
-        bool p_more = true;
-        int p_j = 0, p_blk, p_units, p_t0, p_end, p_id = -1, p_stage = 0;
-        uint32_t holes = 0;                              // stages whose block is not there
-        auto p_open = [&]() {
-            p_units = p.count();
-            p_t0 = p.base + p.unit * kNcTokens;
-            p_end = min(p.s.len, p_t0 + p_units * kNcTokens);
-        };
-        auto p_look = [&]() {
-            const int t = p_t0 + kNibBlock * p_blk;
-            if (p_more && t < p_end) p_id = __ldg(A.table + (size_t)p.b * G.max_blocks + (t >> G.page_shift));
-        };
-        auto p_issue = [&]() {
-            if (!p_more) return;
-            const int t = p_t0 + kNibBlock * p_blk;
-            const bool there = t < p_end, good = there && (unsigned)p_id < (unsigned)G.num_pages;
-            const uint32_t bar = raw_full(uw, p_stage);
-            holes = good ? holes & ~(1u << p_stage) : holes | 1u << p_stage;
-            if (lane == 0) {
+    // units of the range, over all its segments
+    int all_units = 0;
+    {
+        NcWalk c = w;
+        do all_units += c.count(); while (c.next(G, A));
+    }
+
+    if (warp == kNcSoftmax / 32 + 1) {
+        // ================= loader: lane x copies the keys' half of block x of unit n, lane 8 + x the values' half of
+        // unit n - 1, each with a walk of its own
+        if (lane < 2 * kNcBlocks) {
+            const int z = lane / kNcBlocks, x = lane % kNcBlocks;
+            const uint32_t full = raw_full(z), dst = sbase + L::kRaw + (uint32_t)lane * (L::kBlock / 2);
+            bool ok = true;
+            int t, left_units, end, id = -1;
+            const uint8_t* from;                         // of the kv-head in page 0
+            auto open = [&]() {
+                left_units = w.count();
+                t = w.base + w.unit * kNcTokens + kNibBlock * x;
+                end = min(w.s.len, w.base + (w.unit + left_units) * kNcTokens);
+                from = A.pool + (size_t)w.h * G.per * L::kBlock + z * (L::kBlock / 2);
+            };
+            auto look = [&]() {
+                if (t < end) id = __ldg(A.table + (size_t)w.b * G.max_blocks + (t >> G.page_shift));
+            };
+            open();
+            look();
+            for (int n = 0; n < all_units; ++n) {
+                if (n > 0 && !wait(raw_empty(z), (uint32_t)(n - 1) & 1u)) { ok = false; break; }
+                const bool there = t < end, good = there && (unsigned)id < (unsigned)G.num_pages;
+                raw_left[lane] = (uint8_t)(good ? min(kNibBlock, end - t) : 0);
+                if (z == 0) lost_at[(n & 7) * kNcBlocks + x] = good ? 0 : 1;
                 if (good) {
-                    mbar_arrive_expect_tx(bar, L::kBlock);
-                    bulk_g2s(sbase + L::kRaw + (uint32_t)(uw * kNcRawStages + p_stage) * L::kBlock,
-                             A.pool + nib_block_at(G, p_id, p.h, t & (G.page - 1)), L::kBlock, bar);
+                    mbar_arrive_expect_tx(full, L::kBlock / 2);
+                    bulk_g2s(dst, from + (size_t)id * G.page_bytes + (size_t)((t & (G.page - 1)) >> 4) * L::kBlock, L::kBlock / 2, full);
                 } else {
-                    mbar_arrive(bar);
-                    if (there) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)p.b, (uint32_t)p_id);
+                    mbar_arrive(full);
+                    if (there) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)w.b, (uint32_t)id);
                 }
+                t += kNcTokens;
+                if (--left_units == 0 && w.next(G, A)) open();
+                look();
             }
-            p_stage = p_stage + 1 == kNcRawStages ? 0 : p_stage + 1;
-            p_blk += kNcUnpackWarps;
-            if (p_blk >= kNcBlocks) {
-                ++p_j;
-                p_blk = (uw + p_j) % kNcUnpackWarps;
-                p_t0 += kNcTokens;
-                if (--p_units == 0) {
-                    p_more = p.next(G, A);
-                    if (p_more) p_open();
-                }
-            }
-            p_look();
-        };
-        p_blk = uw % kNcUnpackWarps;
-        p_open();
-        p_look();
-        for (int s = 0; s < kNcRawStages; ++s) p_issue();
-        // One block's keys (z = 0) or values into rows row0 .. row0 + 15 of a tile; `left`: its tokens that
-        // exist (the bytes behind them are not to be believed).  Eight lanes take one 32-channel chunk of eight
-        // tokens: all stores, and the loads of values, fall in distinct banks.  All loads come before the
-        // first store, which the compiler could not know to be elsewhere.
-        auto unpack = [&](int z, const uint8_t* blk, uint8_t* tile, int row0, int left) {
-            constexpr int kIts = D / 64;
-            uint4 cw[kIts];
-            uint32_t s0[kIts], s1[kIts];
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-                const int q = it * 4 + (lane >> 3), t = (lane & 7) + 8 * (q & 1), c = q >> 1;    // (token half, chunk)
-                cw[it] = make_uint4(0, 0, 0, 0);
-                s0[it] = s1[it] = 0;
-                if (t < left) {
-                    cw[it] = *reinterpret_cast<const uint4*>(blk + (z ? nib_v_off(D, t, 16 * c) : nib_k_off(D, t) + 16 * c));
-                    s0[it] = blk[z ? nib_vscale_off(D, t, 2 * c) : nib_kscale_off(D, t, 2 * c)];
-                    s1[it] = blk[z ? nib_vscale_off(D, t, 2 * c + 1) : nib_kscale_off(D, t, 2 * c + 1)];
-                }
-            }
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-                const int q = it * 4 + (lane >> 3), t = (lane & 7) + 8 * (q & 1), c = q >> 1;
-                const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
-                const uint32_t r0 = 0x00800080u * s0[it], r1 = 0x00800080u * s1[it];
-                const uint32_t b00 = hmul2_(r0, kNibB0), b01 = hmul2_(r0, kNibB1), b10 = hmul2_(r1, kNibB0), b11 = hmul2_(r1, kNibB1);
-                uint8_t* dst = tile + (c >> 1) * L::kHalf + (row0 + t) * 128;
-                uint32_t o[4][4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) nib_unpack(words[y], y < 2 ? r0 : r1, y < 2 ? b00 : b10, y < 2 ? b01 : b11, e8, eh, o[y]);
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + y) ^ (t & 7)) << 4)) = make_uint4(o[y][0], o[y][1], o[y][2], o[y][3]);
-            }
-        };
-        int stage = 0;
-        uint32_t phase = 0, j = 0;                       // j: units so far
-        bool ok = true;
-        for (bool some = true; ok && some; some = w.next(G, A)) {
-            const int cnt = w.count();
-            for (int u = 0; ok && u < cnt; ++u, ++j) {
-                const int buf = j & 1, first = (int)((uw + j) % kNcUnpackWarps);
-                const int end = w.s.len - (w.base + (w.unit + u) * kNcTokens);       // tokens that exist, from the unit's first on
-                const uint32_t before = ((j >> 1) - 1) & 1u;
-                uint32_t lost = 0;
-                // the keys of the warp's blocks, then their values: the scores are waited for first.  A
-                // buffer is free when the products that read it two units ago are done
-                ok = j < 2 || wait(k_empty(buf), before);
-                int st = stage;
-                uint32_t ph = phase;
-#pragma unroll 1
-                for (int x = first; ok && x < kNcBlocks; x += kNcUnpackWarps) {
-                    if (!wait(raw_full(uw, st), ph)) { ok = false; break; }
-                    const bool gone = (holes >> st) & 1u;
-                    lost |= (uint32_t)gone << x;
-                    unpack(0, sm + L::kRaw + (uw * kNcRawStages + st) * L::kBlock, sm + L::kK + buf * L::kTile, kNibBlock * x,
-                           gone ? 0 : end - kNibBlock * x);
-                    if (++st == kNcRawStages) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                }
-                if (!ok) break;
-                if (lane == 0) k_flags[(j & 3u) * 4 + uw] = (uint8_t)lost;
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(k_full(buf));
-                if (j >= 2 && !wait(v_empty(buf), before)) { ok = false; break; }
-#pragma unroll 1
-                for (int x = first; x < kNcBlocks; x += kNcUnpackWarps) {
-                    unpack(1, sm + L::kRaw + (uw * kNcRawStages + stage) * L::kBlock, sm + L::kV + buf * L::kTile, kNibBlock * x,
-                           (lost >> x) & 1u ? 0 : end - kNibBlock * x);
-                    __syncwarp();                        // the block is read: its stage takes another
-                    p_issue();
-                    if (++stage == kNcRawStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_full(buf));
-            }
+            if (!ok) mbar_wait_for(full, 0u, 10000000ull), mbar_wait_for(full, 1u, 10000000ull);   // what is in flight, within a limit
         }
-        if (!ok)                                         // the copies in flight end first, each wait with a limit
-            for (int k = 0; k < kNcRawStages; ++k)
-                mbar_wait_for(raw_full(uw, (stage + k) % kNcRawStages), phase ^ (uint32_t)(stage + k >= kNcRawStages), 10000000ull);
-    } else if (warp == kNcSoftmax / 32 + kNcUnpackWarps) {
+        __syncwarp();
+    } else if (warp == kNcSoftmax / 32) {
         // ================= MMA: one thread
         if (lane == 0) {
             bool ok = true, any = false;
@@ -462,7 +379,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 const uint32_t vb = sbase + L::kV + (jj & 1) * L::kTile;
 #pragma unroll
                 for (int k = 0; k < kNcTokens / 16; ++k)
-                    nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + 8 * k, nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
+                    nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + (k >> 2) * 64 + 8 * (k & 3), nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
                               start && k == 0 ? 0u : 1u);
             };
             auto after = [&](bool got) {
@@ -504,18 +421,77 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
         // ================= softmax: a thread a row of tile t
         // A wait that ran out leaves ok false: the loops run to their end without waiting or issuing, so
         // that every thread meets the others at the barriers.
-        const int t = warp >> 2, r = tid & (kNcRows - 1);
-        const bool leader = r == 0;
+        const int t = warp >> 3, hc = (warp >> 2) & 1, r = tid & (kNcRows - 1);   // tile, its tokens' (and O's channels') half, row
+        const bool leader = (tid & (kNcTile - 1)) == 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // this warp's tensor-memory lanes (32 of 128, bits 16 up)
-        const uint32_t s_at = tmem + lanes + kTmS + t * 128, o_at = tmem + lanes + kTmO + t * D;
+        const uint32_t s_at = tmem + lanes + kTmS + t * 128 + hc * 64, o_at = tmem + lanes + kTmO + t * D + hc * (D / 2);
+        float* ex = reinterpret_cast<float*>(sm + L::kEx) + t * 2 * kNcRows;       // [2][2 tiles][2 halves][rows]
         uint32_t j = 0, items = 0, units = 0, segs = 0;  // units and segments of this tile, of the CTA
         bool ok = true;
+        const uint32_t e8 = reg_const(0x48004800u), eh = reg_const(0x38003800u);
+        // This warp's block of unit n, keys (z = 0) or values, into its rows of the operand tile; bytes behind the last
+        // token are not to be believed.  Eight lanes take one 32-channel chunk of eight tokens: all stores, and the
+        // loads of values, fall in distinct banks.  All loads come before the first store, which the compiler could
+        // not know to be elsewhere.
+        const int blk_of = warp & (kNcBlocks - 1);
+        auto unpack_as = [&](auto zz, uint32_t n) {
+            constexpr int z = decltype(zz)::value;
+            if (n >= (uint32_t)all_units) return;
+            // the products that read this buffer two units ago are done, and the bytes are there
+            if (ok && n >= 2) ok = wait(z ? v_empty(n & 1) : k_empty(n & 1), ((n >> 1) - 1) & 1u);
+            if (ok) ok = wait(raw_full(z), n & 1u);
+            constexpr int kIts = D / 64;
+            const uint8_t* blk = sm + L::kRaw + (z * kNcBlocks + blk_of) * (L::kBlock / 2) - z * (L::kBlock / 2);   // as if the whole block were there
+            const int left = raw_left[z * kNcBlocks + blk_of];
+            uint4 cw[kIts];
+            uint32_t s0[kIts], s1[kIts];
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int q = it * 4 + (lane >> 3), tk = (lane & 7) + 8 * (q & 1), c = q >> 1;   // (token half, chunk)
+                cw[it] = make_uint4(0, 0, 0, 0);
+                s0[it] = s1[it] = 0;
+                if (tk < left) {
+                    cw[it] = *reinterpret_cast<const uint4*>(blk + (z ? nib_v_off(D, tk, 16 * c) : nib_k_off(D, tk) + 16 * c));
+                    s0[it] = blk[z ? nib_vscale_off(D, tk, 2 * c) : nib_kscale_off(D, tk, 2 * c)];
+                    s1[it] = blk[z ? nib_vscale_off(D, tk, 2 * c + 1) : nib_kscale_off(D, tk, 2 * c + 1)];
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int q = it * 4 + (lane >> 3), tk = (lane & 7) + 8 * (q & 1), c = q >> 1;
+                const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
+                const uint32_t r0 = 0x00800080u * s0[it], r1 = 0x00800080u * s1[it];
+                const uint32_t b00 = hmul2_(r0, kNibB0), b01 = hmul2_(r0, kNibB1), b10 = hmul2_(r1, kNibB0), b11 = hmul2_(r1, kNibB1);
+                uint8_t* dst = sm + (z ? L::kV : L::kK) + (n & 1) * L::kTile + (c >> 1) * L::kHalf + (kNibBlock * blk_of + tk) * 128;
+                uint32_t o[4][4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) nib_unpack(words[y], y < 2 ? r0 : r1, y < 2 ? b00 : b10, y < 2 ? b01 : b11, e8, eh, o[y]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + y) ^ (tk & 7)) << 4)) = make_uint4(o[y][0], o[y][1], o[y][2], o[y][3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && ok) {
+                mbar_arrive(raw_empty(z));
+                mbar_arrive(z ? v_full(n & 1) : k_full(n & 1));
+            }
+        };
+        // what the tile's warps prepare after unit n: keys two units ahead, or values one
+        auto unpack = [&](uint32_t n) {
+            if (t == 0) unpack_as(std::integral_constant<int, 0>{}, n + 2);
+            else unpack_as(std::integral_constant<int, 1>{}, n + 1);
+        };
+        if (t == 0) unpack_as(std::integral_constant<int, 0>{}, 0);
+        unpack(0u - 1u);
         for (bool some = true; some; some = w.next(G, A)) {
             const int cnt = w.count(), rows = w.s.nq * G.g, row = 2 * kNcRows * w.x + kNcRows * t + r;
             const int tiles = rows - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
             if (t >= tiles) {                            // no such tile; the queries' barrier counts all the same
                 mbar_arrive(q_ready);
-                units += cnt;
+                for (int u = 0; u < cnt; ++u, ++units) {
+                    unpack(units);
+                }
                 at += w.step();
                 // the next arrival belongs to the next segment: not before this one has begun
                 if (ok) ok = wait(q_ready, segs & 1u);
@@ -545,7 +521,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 fac = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
                 uint8_t* dst = sm + L::kQ + t * L::kTile + r * 128;
 #pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
+                for (int c = hc * (D / 16); c < (hc + 1) * (D / 16); ++c) {          // half the row a thread
                     const uint4 v = have ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
                     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
                     float f[8];
@@ -582,54 +558,48 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 if (ok) ok = wait(s_full(t), j & 1u);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const int t0 = w.base + (w.unit + u) * kNcTokens;
-                uint32_t lost = *reinterpret_cast<const uint32_t*>(k_flags + (units & 3u) * 4);
-                lost |= lost >> 8 | lost >> 16;          // a bit a block
-                const bool part = t0 + kNcTokens - 1 > all_hi || t0 < all_lo || (lost & 255u);
-                uint32_t pk[kNcTokens / 2];
-                float sum, top;
-                for (bool again = false;;) {             // a second time when the maximum moves
-                    const float2 c0 = make_float2(kNdBias - m, kNdBias - m), f2 = make_float2(fac, fac);
-                    float2 sums[4];
-                    float tops[4];
+                const uint2 lost = *reinterpret_cast<const uint2*>(lost_at + (units & 7u) * kNcBlocks);   // a byte a block
+                const bool part = t0 + kNcTokens - 1 > all_hi || t0 < all_lo || (lost.x | lost.y);
+                // the half's tokens that this row sees
+                uint32_t seen[2] = {~0u, ~0u};
+                if (part) {
+                    const uint32_t gone = hc ? lost.y : lost.x;
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        sums[y] = make_float2(0.f, 0.f);
-                        tops[y] = -INFINITY;
+                    for (int c = 0; c < 2; ++c) seen[c] = seen_of(t0 + 64 * hc + 32 * c, (gone >> (16 * c) & 1u) | (gone >> (16 * c + 8) & 1u) << 1);
+                }
+                auto mask = [&](float (&x)[32], int c) {
+                    if (part) {
+                        asm volatile("" ::: "memory");
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) x[y] = (seen[c] >> y) & 1u ? x[y] : -INFINITY;
                     }
-                    float v[2][32];
-                    nc_ld32_issue(s_at, v[0]);
+                };
+                float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {        // the next columns come while these are worked on
-                        float (&x)[32] = v[c & 1];
-                        nc_ld_wait(x);
-                        if (c < 3) nc_ld32_issue(s_at + 32 * (c + 1), v[(c + 1) & 1]);
-                        if (part) {
-                            asm volatile("" ::: "memory");
-                            const uint32_t seen = seen_of(t0 + 32 * c, lost >> (2 * c));
+                for (int c = 0; c < 2; ++c) {
+                    float x[32];
+                    nc_ld32(s_at + 32 * c, x);
+                    mask(x, c);
+                    float tops[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) x[y] = (seen >> y) & 1u ? x[y] : -INFINITY;
-                        }
+                    for (int y = 4; y < 32; y += 4)
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) {
-                            tops[(y >> 1) & 3] = fmaxf(tops[(y >> 1) & 3], fmaxf(x[y], x[y + 1]));
-                            const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
-                            const float2 p = make_float2(ex2(z.x), ex2(z.y));
-                            sums[(y >> 1) & 3] = add2(sums[(y >> 1) & 3], p);
-                            pk[16 * c + y / 2] = pack_half2(p.x, p.y);
-                        }
-                    }
-                    const float2 sa = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
-                    sum = sa.x + sa.y;
-                    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    const float mx = top > -INFINITY ? top * fac : kNdNone;
-                    if (again || !__any_sync(~0u, mx > m + kNdLag)) break;
-                    again = true;
+                        for (int z = 0; z < 4; ++z) tops[z] = fmaxf(tops[z], x[y + z]);
+                    top = fmaxf(top, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+                }
+                // the row's other half; two places in turn, so that one barrier a unit will do
+                float* place = ex + (units & 1u) * 4 * kNcRows;
+                place[hc * kNcRows + r] = top;
+                named_barrier(1 + t, kNcTile);
+                top = fmaxf(top, place[(hc ^ 1) * kNcRows + r]);
+                const float mx = top > -INFINITY ? top * fac : kNdNone;
+                if (__any_sync(~0u, mx > m + kNdLag)) {
                     const float mn = fmaxf(m, mx), f = ex2(m - mn);
                     m = mn;
                     l *= f;
                     if (u > 0) {                         // O holds the units before: these scores came after their products
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
+                        for (int c = 0; c < D / 64; ++c) {
                             float o[32];
                             nc_ld32(o_at + 32 * c, o);
                             uint32_t ou[32];
@@ -639,17 +609,41 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                         }
                     }
                 }
-                l += sum;
+                const float2 c0 = make_float2(kNdBias - m, kNdBias - m), f2 = make_float2(fac, fac);
+                float2 sums[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x[32];
+                    nc_ld32(s_at + 32 * c, x);
+                    mask(x, c);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2) {
+                        const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
+                        const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                        sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
+                        pk[16 * c + y / 2] = pack_half2(p.x, p.y);
+                    }
+                }
+                const float2 sa = add2(sums[0], sums[1]);
+                l = sa.x + sa.y;
                 nc_st32(s_at, pk);
-                nc_st32(s_at + 32, pk + 32);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 mbar_arrive(p_ready(t));
+                unpack(units);
             }
             // ---- the segment ends
             if (ok) ok = wait(o_full(t), items & 1u);
             ++items;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            // the row's sum, over both halves (the places that the last unit's maxima did not use)
+            {
+                float* place = ex + (units & 1u) * 4 * kNcRows;
+                place[hc * kNcRows + r] = l;
+                named_barrier(1 + t, kNcTile);
+                l += place[(hc ^ 1) * kNcRows + r];
+            }
             const bool whole = w.unit == 0 && cnt == w.real();
             const long long first = at - w.unit;
             const size_t out_at = (size_t)(row0 + jq) * G.hq + (size_t)(w.h * G.g + hg);
@@ -676,30 +670,33 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * L::kRec + (size_t)t * kNcRows * (D + 2);
                 const float inv = l > 0.f ? 32.f / l : 0.f;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D / 64; ++c) {
+                    const int c32 = hc * (D / 64) + c;   // 32 channels
                     float v[32];
                     nc_ld32(o_at + 32 * c, v);
                     if (whole) {
                         if (have) {
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) put8(4 * c + y, v + 8 * y, inv);
+                            for (int y = 0; y < 4; ++y) put8(4 * c32 + y, v + 8 * y, inv);
                         }
                     } else {                             // [m][l][D / 4] of 128 rows each: rows side by side
 #pragma unroll
                         for (int y = 0; y < 8; ++y)
-                            *reinterpret_cast<float4*>(rec + 2 * kNcRows + (size_t)((8 * c + y) * kNcRows + r) * 4) =
+                            *reinterpret_cast<float4*>(rec + 2 * kNcRows + (size_t)((8 * c32 + y) * kNcRows + r) * 4) =
                                 make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
                     }
                 }
-                if (whole) {
-                    if (have) put_lse(m, l);
-                } else {
-                    rec[r] = m;
-                    rec[kNcRows + r] = l;
+                if (hc == 0) {
+                    if (whole) {
+                        if (have) put_lse(m, l);
+                    } else {
+                        rec[r] = m;
+                        rec[kNcRows + r] = l;
+                    }
                 }
             }
             if (!whole) {                                // the last CTA of this item merges the records
-                named_barrier(1 + t, kNcRows);
+                named_barrier(1 + t, kNcTile);
                 if (leader) {                            // the barrier, then one fence: the whole tile's record is out
                     __threadfence();
                     const int c0 = cta_of(first), c1 = cta_of(first + w.real() - 1);
@@ -710,7 +707,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     if (k == c1 - c0) A.tickets[2 * c0 + t] = 0;
                     __threadfence();
                 }
-                named_barrier(1 + t, kNcRows);
+                named_barrier(1 + t, kNcTile);
                 if (s_last[t][0] && have) {
                     const int c0 = s_last[t][1], c1 = s_last[t][2];
                     const int slot0 = first == total * c0 / ctas ? 0 : 1;
@@ -722,7 +719,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     for (int c = c0; c <= c1; ++c) ll = fmaf(ex2(__ldcg(record(c) + r) - mm), __ldcg(record(c) + kNcRows + r), ll);
                     const float inv = ll > 0.f ? 32.f / ll : 0.f;
 #pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
+                    for (int q = hc * (D / 32); q < (hc + 1) * (D / 32); ++q) {
                         float v[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) v[y] = 0.f;
@@ -742,9 +739,9 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                         put8(2 * q, v, inv);
                         put8(2 * q + 1, v + 8, inv);
                     }
-                    put_lse(mm, ll);
+                    if (hc == 0) put_lse(mm, ll);
                 }
-                named_barrier(1 + t, kNcRows);           // s_last is read
+                named_barrier(1 + t, kNcTile);           // s_last is read
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             at += w.step();

@@ -100,8 +100,8 @@ struct NibAttend {
 
 cudaError_t nib_prepare_store();
 cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s);
-cudaError_t nib_append(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s);
-cudaError_t nib_read(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s);
+cudaError_t nib_append(const NibGeom& G, const NibRows& R, cudaStream_t s);
+cudaError_t nib_read(const NibGeom& G, const NibRows& R, cudaStream_t s);
 // Bytes of the handle's arena behind its first 256 (the error word): tickets, records.
 size_t nib_attend_bytes(int d);
 cudaError_t nib_prepare_attend(const NibGeom& G);

@@ -224,7 +224,7 @@ dwkv_status dwkv_nibble_append(dwkv_nibble_handle h, int32_t n_rows, const void*
     NIB_DEVICE(h);
     const NibRows R{n_rows, k_stride, v_stride, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), slots,
                     static_cast<uint8_t*>(pool), nullptr, nullptr};
-    const cudaError_t e = nib_append(h->geom, R, h->num_sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = nib_append(h->geom, R, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "dwkv_nibble_append launch");
     return DWKV_OK;
 }
@@ -240,7 +240,7 @@ dwkv_status dwkv_nibble_read(dwkv_nibble_handle h, int32_t n_rows, const int32_t
     NIB_DEVICE(h);
     const NibRows R{n_rows, w, w, nullptr, nullptr, slots, static_cast<uint8_t*>(const_cast<void*>(pool)),
                     static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out)};
-    const cudaError_t e = nib_read(h->geom, R, h->num_sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = nib_read(h->geom, R, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "dwkv_nibble_read launch");
     return DWKV_OK;
 }

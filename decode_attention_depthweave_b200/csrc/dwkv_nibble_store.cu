@@ -1,7 +1,5 @@
 // dwkv_nibble_store.cu -- the 4-bit cache's tables (which pages a request holds, where its new
 // rows go), append (quantise rows into their slots) and read (the stored values).
-#include <algorithm>
-
 #include "dwkv_nibble.cuh"
 
 namespace dwkv {
@@ -192,8 +190,13 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
 }
 
 // ------------------------------------------------------------------------------------
-// Append: a lane quantises 8 channels of one vector (one 16-byte load), two lanes a block of 16.
+// Append and read: a warp a row of keys or of values, a lane 8 channels of a head (one 16-byte load or
+// store), two lanes a block of 16; kAhead heads' loads are issued before the first is used.  Bound by the
+// bytes of the 16-bit rows (512 of 656 a token and kv-head at d = 128).
 // ------------------------------------------------------------------------------------
+constexpr int kRowWarps = 8;
+constexpr int kAhead = 4;
+
 // e5m3 byte of y >= 0 (finite): RNE of y to 4 significant bits (to multiples of 2^-17 below 2^-14).
 __device__ __forceinline__ uint32_t e5m3_of(float y) {
     y = fminf(y, kNibScaleMax);
@@ -203,91 +206,126 @@ __device__ __forceinline__ uint32_t e5m3_of(float y) {
     return u - ((127u - 15u) << 3);
 }
 
-template <bool FP16>
-__global__ void __launch_bounds__(256) nib_append_kernel(const NibGeom G, const NibRows R) {
-    const int d = G.d, lv = d >> 3;                                           // lanes of a vector
-    const long long total = (long long)R.n * G.hkv * 2 * lv;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
-        const int part = (int)(i % lv);
-        const long long vec = i / lv;
-        const int h = (int)(vec % G.hkv);
-        const long long rz = vec / G.hkv;
-        const int z = (int)(rz & 1);
-        const int row = (int)(rz >> 1);
-        const int slot = R.slots[row];
-        const uint16_t* src = (z ? R.v + row * R.v_stride : R.k + row * R.k_stride) + h * d + part * 8;
-        float x[8];
-        float a = 0.f;
-        bool odd = false;
-        const uint4 w = *reinterpret_cast<const uint4*>(src);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+// The row and slot of a warp; false where there is nothing to do (slot -1: `skip`).
+struct NibRow {
+    int row, z, slot, tok;
+    uint8_t* base;                               // of the slot's block of head 0
+};
+__device__ __forceinline__ bool nib_row(const NibGeom& G, const NibRows& R, NibRow& x) {
+    const long long w = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    x.row = (int)(w >> 1);
+    x.z = (int)(w & 1);
+    x.slot = -1;
+    if (x.row >= R.n) return false;
+    x.slot = __ldg(R.slots + x.row);
+    if ((unsigned)x.slot >= (unsigned)G.num_pages * (unsigned)G.page) {
+        if (x.slot != -1 && (threadIdx.x & 31) == 0) nib_error(G, 12u /*DWKV_DEV_BAD_SLOT*/, (uint32_t)x.row, (uint32_t)x.slot);
+        x.slot = -1;
+        return true;
+    }
+    x.tok = x.slot & (G.page - 1);
+    x.base = R.pool + nib_block_at(G, x.slot >> G.page_shift, 0, x.tok);
+    return true;
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(32 * kRowWarps) nib_append_kernel(const NibGeom G, const NibRows R) {
+    constexpr int LV = D / 8, HS = 32 / LV;                       // lanes of a vector, heads side by side
+    NibRow x;
+    if (!nib_row(G, R, x) || x.slot < 0) return;
+    const int lane = threadIdx.x & 31, part = lane % LV, t = x.tok & 15;
+    const uint16_t* src = (x.z ? R.v + x.row * R.v_stride : R.k + x.row * R.k_stride) + part * 8;
+    const uint32_t at = x.z ? nib_v_off(D, t, 4 * part) : nib_k_off(D, t) + 4 * part;
+    const uint32_t at_s = x.z ? nib_vscale_off(D, t, part >> 1) : nib_kscale_off(D, t, part >> 1);
+    const size_t head_bytes = (size_t)G.per * G.blk;
+    for (int h0 = lane / LV; h0 < G.hkv; h0 += HS * kAhead) {
+        uint4 in[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = (ws[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-            float f = FP16 ? __half2float(__ushort_as_half((unsigned short)b)) : __uint_as_float(b << 16);
-            odd |= !(fabsf(f) <= 7.f * kNibScaleMax);
-            f = f != f ? 0.f : fminf(fmaxf(f, -7.f * kNibScaleMax), 7.f * kNibScaleMax);
-            x[j] = f;
-            a = fmaxf(a, fabsf(f));
-        }
-        // the two lanes of a block are neighbours (total is a multiple of 8)
-        a = fmaxf(a, __shfl_xor_sync(3u << (threadIdx.x & 30u), a, 1));
-        const uint32_t sb = e5m3_of(__fdiv_rn(a, 7.f));
-        const float s = nib_scale((uint8_t)sb);
-        uint32_t u = 0;
+        for (int k = 0; k < kAhead; ++k)
+            in[k] = h0 + k * HS < G.hkv ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(h0 + k * HS) * D)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = sb ? max(-7, min(7, __float2int_rn(__fdiv_rn(x[j], s)))) : 0;
-            u |= (uint32_t)(c + 8) << (4 * j);
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = h0 + k * HS;
+            const uint32_t ws[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+            float f[8], a = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = (ws[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+                f[j] = FP16 ? __half2float(__ushort_as_half((unsigned short)b)) : __uint_as_float(b << 16);
+                a = fmaxf(a, fabsf(f[j]));
+            }
+            // NaN, infinite or beyond the largest value (rare): NaN to 0, the rest clamped
+            bool odd = a > 7.f * kNibScaleMax;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) odd |= f[j] != f[j];
+            if (odd) {
+                a = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f[j] = f[j] != f[j] ? 0.f : fminf(fmaxf(f[j], -7.f * kNibScaleMax), 7.f * kNibScaleMax);
+                    a = fmaxf(a, fabsf(f[j]));
+                }
+                nib_error(G, 9u /*DWKV_DEV_RANGE*/, (uint32_t)x.row, (uint32_t)(2 * h + x.z));
+            }
+            // the two lanes of a block are neighbours, of one head: both are here
+            a = fmaxf(a, __shfl_xor_sync(3u << (lane & 30), a, 1));
+            if (h >= G.hkv) continue;
+            const uint32_t sb = e5m3_of(__fdiv_rn(a, 7.f));
+            const float s = nib_scale((uint8_t)sb), r = sb ? __frcp_rn(s) : 0.f;
+            uint32_t u = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // rint(f / s), ties to even, without a division: n is the nearest whole number to f (1/s) (two
+                // roundings, so it may be either one at a tie), e = f - n s is exact, and |e| = s / 2 is a tie
+                float n = rintf(f[j] * r);
+                const float e = fmaf(-n, s, f[j]);
+                if (fabsf(e) == 0.5f * s && (__float2int_rn(n) & 1)) n += copysignf(1.f, e);
+                const int c = max(-7, min(7, __float2int_rn(n)));
+                u |= (uint32_t)(c + 8) << (4 * j);
+            }
+            // each 16-bit unit rotated left by 2
+            u = ((u << 2) & 0xfffcfffcu) | ((u >> 14) & 0x00030003u);
+            uint8_t* blk = x.base + h * head_bytes;
+            *reinterpret_cast<uint32_t*>(blk + at) = u;
+            if (!(part & 1)) blk[at_s] = (uint8_t)sb;
         }
-        // each 16-bit unit rotated left by 2
-        u = ((u << 2) & 0xfffcfffcu) | ((u >> 14) & 0x00030003u);
-        if (slot == -1) continue;
-        if ((unsigned)slot >= (unsigned)G.num_pages * (unsigned)G.page) {
-            nib_error(G, 12u /*DWKV_DEV_BAD_SLOT*/, (uint32_t)row, (uint32_t)slot);
-            continue;
-        }
-        if (odd) nib_error(G, 9u /*DWKV_DEV_RANGE*/, (uint32_t)row, (uint32_t)(2 * h + z));
-        const int tok = slot % G.page, t = tok & 15;
-        uint8_t* blk = R.pool + nib_block_at(G, slot / G.page, h, tok);
-        *reinterpret_cast<uint32_t*>(blk + (z ? nib_v_off(d, t, 4 * part) : nib_k_off(d, t) + 4 * part)) = u;
-        if (!(part & 1)) blk[z ? nib_vscale_off(d, t, part >> 1) : nib_kscale_off(d, t, part >> 1)] = (uint8_t)sb;
     }
 }
 
 // The stored values of the given slots (zeros for -1), in the caller's 16-bit type: exact.
-template <bool FP16>
-__global__ void __launch_bounds__(256) nib_read_kernel(const NibGeom G, const NibRows R) {
-    const int d = G.d, lv = d >> 3;
-    const long long total = (long long)R.n * G.hkv * 2 * lv;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
-        const int part = (int)(i % lv);
-        const long long vec = i / lv;
-        const int h = (int)(vec % G.hkv);
-        const long long rz = vec / G.hkv;
-        const int z = (int)(rz & 1);
-        const int row = (int)(rz >> 1);
-        const int slot = R.slots[row];
-        uint32_t o[4] = {0, 0, 0, 0};
-        if (slot != -1) {
-            if ((unsigned)slot >= (unsigned)G.num_pages * (unsigned)G.page) {
-                nib_error(G, 12u, (uint32_t)row, (uint32_t)slot);
-            } else {
-                const int tok = slot % G.page, t = tok & 15;
-                const uint8_t* blk = R.pool + nib_block_at(G, slot / G.page, h, tok);
-                uint32_t u = *reinterpret_cast<const uint32_t*>(blk + (z ? nib_v_off(d, t, 4 * part) : nib_k_off(d, t) + 4 * part));
-                const float s = nib_scale(blk[z ? nib_vscale_off(d, t, part >> 1) : nib_kscale_off(d, t, part >> 1)]);
-                u = ((u >> 2) & 0x3fff3fffu) | ((u & 0x00030003u) << 14);
+template <int D, bool FP16>
+__global__ void __launch_bounds__(32 * kRowWarps) nib_read_kernel(const NibGeom G, const NibRows R) {
+    constexpr int LV = D / 8, HS = 32 / LV;
+    NibRow x;
+    if (!nib_row(G, R, x)) return;
+    const int lane = threadIdx.x & 31, part = lane % LV, t = x.tok & 15;
+    uint16_t* dst = (x.z ? R.v_out : R.k_out) + (size_t)x.row * G.hkv * D + part * 8;
+    const uint32_t at = x.z ? nib_v_off(D, t, 4 * part) : nib_k_off(D, t) + 4 * part;
+    const uint32_t at_s = x.z ? nib_vscale_off(D, t, part >> 1) : nib_kscale_off(D, t, part >> 1);
+    const size_t head_bytes = (size_t)G.per * G.blk;
+    for (int h0 = lane / LV; h0 < G.hkv; h0 += HS * kAhead) {
+        uint32_t u[kAhead], sb[kAhead];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float f = (float)((int)((u >> (4 * j)) & 15u) - 8) * s;
-                    const uint32_t b = FP16 ? (uint32_t)__half_as_ushort(__float2half_rn(f)) : __float_as_uint(f) >> 16;
-                    o[j >> 1] |= b << (16 * (j & 1));
-                }
-            }
+        for (int k = 0; k < kAhead; ++k) {
+            const bool in = x.slot >= 0 && h0 + k * HS < G.hkv;
+            const uint8_t* blk = x.base + (h0 + k * HS) * head_bytes;
+            u[k] = in ? *reinterpret_cast<const uint32_t*>(blk + at) : 0x22222222u;      // codes 0
+            sb[k] = in ? blk[at_s] : 0u;
         }
-        uint16_t* dst = (z ? R.v_out : R.k_out) + ((size_t)row * G.hkv + h) * d + part * 8;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (h0 + k * HS >= G.hkv) break;
+            const float s = nib_scale((uint8_t)sb[k]);
+            const uint32_t v = ((u[k] >> 2) & 0x3fff3fffu) | ((u[k] & 0x00030003u) << 14);
+            uint32_t o[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f = x.slot >= 0 ? (float)((int)((v >> (4 * j)) & 15u) - 8) * s : 0.f;
+                const uint32_t b = FP16 ? (uint32_t)__half_as_ushort(__float2half_rn(f)) : __float_as_uint(f) >> 16;
+                o[j >> 1] |= b << (16 * (j & 1));
+            }
+            *reinterpret_cast<uint4*>(dst + (size_t)(h0 + k * HS) * D) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
 }
 
@@ -311,20 +349,19 @@ cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s) {
     return cudaLaunchKernelEx(&c, nib_tables_kernel, G, T);
 }
 
-static unsigned row_grid(const NibGeom& G, const NibRows& R, int sms) {
-    const long long lanes = (long long)R.n * G.hkv * 2 * (G.d >> 3);
-    return (unsigned)std::max(1ll, std::min((lanes + 255) / 256, 8ll * sms));
-}
+static unsigned row_grid(const NibRows& R) { return (unsigned)((2ll * R.n + kRowWarps - 1) / kRowWarps); }
 
-cudaError_t nib_append(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s) {
-    if (G.fp16) nib_append_kernel<true><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
-    else nib_append_kernel<false><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
+cudaError_t nib_append(const NibGeom& G, const NibRows& R, cudaStream_t s) {
+    auto k = G.d == 128 ? (G.fp16 ? nib_append_kernel<128, true> : nib_append_kernel<128, false>)
+                        : (G.fp16 ? nib_append_kernel<64, true> : nib_append_kernel<64, false>);
+    k<<<row_grid(R), 32 * kRowWarps, 0, s>>>(G, R);
     return cudaGetLastError();
 }
 
-cudaError_t nib_read(const NibGeom& G, const NibRows& R, int sms, cudaStream_t s) {
-    if (G.fp16) nib_read_kernel<true><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
-    else nib_read_kernel<false><<<row_grid(G, R, sms), 256, 0, s>>>(G, R);
+cudaError_t nib_read(const NibGeom& G, const NibRows& R, cudaStream_t s) {
+    auto k = G.d == 128 ? (G.fp16 ? nib_read_kernel<128, true> : nib_read_kernel<128, false>)
+                        : (G.fp16 ? nib_read_kernel<64, true> : nib_read_kernel<64, false>);
+    k<<<row_grid(R), 32 * kRowWarps, 0, s>>>(G, R);
     return cudaGetLastError();
 }
 

@@ -130,6 +130,11 @@ def _raw(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# cudaStream_t of a device's current stream, without building a Stream object where torch allows it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class Nibble:
     """One handle on tensors that the caller owns.  Allocates the handle's arena, nothing else
     (and outputs that are not passed in)."""
@@ -143,6 +148,8 @@ class Nibble:
             else torch.device(device)
         self.dtype = torch.float16 if cfg.dtype == DWKV_FP16 else torch.bfloat16
         self.pool_bytes = dwkv_nibble_pool_bytes(cfg)
+        self.index, self.max_blocks, self.head_dim = self.device.index, cfg.max_blocks, cfg.head_dim
+        self.num_q_heads, self.num_kv_heads = cfg.num_q_heads, cfg.num_kv_heads
         with torch.cuda.device(self.device):
             self.arena = torch.empty(dwkv_nibble_arena_bytes(cfg), dtype=torch.uint8, device=self.device)
             self.h = dwkv_nibble_create(cfg, self.arena, stream)
@@ -160,31 +167,39 @@ class Nibble:
 
     # ---- checks of what the C side cannot see: types, devices, extents
     def _ints(self, name, t, n, exact=False):
-        if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or \
-                (t.numel() != n if exact else t.numel() < n):
+        have = t.numel()
+        if t.dtype is not torch.int32 or t.get_device() != self.index or not t.is_contiguous() or \
+                (have != n if exact else have < n):
             raise ValueError(f"{name} must be contiguous int32 on {self.device} with {n} entries "
                              f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
 
     def _table(self, t, n):
-        if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or t.dim() != 2 or \
-                t.shape[0] < n or t.shape[1] != self.cfg.max_blocks:
-            raise ValueError(f"block_tables must be contiguous int32 [>= {n}][{self.cfg.max_blocks}] on {self.device} "
+        if t.dtype is not torch.int32 or t.get_device() != self.index or not t.is_contiguous() or t.dim() != 2 or \
+                t.size(0) < n or t.size(1) != self.max_blocks:
+            raise ValueError(f"block_tables must be contiguous int32 [>= {n}][{self.max_blocks}] on {self.device} "
                              f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
 
     def _pool(self, t):
-        if t.device != self.device or not t.is_contiguous() or t.numel() * t.element_size() != self.pool_bytes:
+        if t.get_device() != self.index or not t.is_contiguous() or t.numel() * t.element_size() != self.pool_bytes:
             raise ValueError(f"pool must be {self.pool_bytes} contiguous bytes on {self.device}")
 
     def _rows(self, name, t, heads):
-        """Row stride of a [rows][heads][head_dim] tensor whose rows are dense."""
-        d = self.cfg.head_dim
-        if t.dtype != self.dtype or t.device != self.device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        """(rows, row stride) of a [rows][heads][head_dim] tensor whose rows are dense."""
+        if t.dtype is not self.dtype or t.get_device() != self.index or t.dim() != 3:
+            shape = ()
+        else:
+            shape = t.shape
+        d = self.head_dim
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d:
             raise ValueError(f"{name} must be {self.dtype} [rows][{heads}][{d}] on {self.device} "
                              f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
         row, head, one = t.stride()
-        if (one != 1 and d > 1) or (head != d and heads > 1):
+        if one != 1 or (head != d and heads > 1):
             raise ValueError(f"{name}: each row's heads must be dense (strides {t.stride()})")
-        return row if t.shape[0] > 1 else heads * d
+        return shape[0], row if shape[0] > 1 else heads * d
+
+    def _stream(self, stream):
+        return _current_stream(self.index) if stream is None else _raw(stream, self.device)
 
     def tables(self, n_new, seq_lens, block_tables, free_list, free_count, cu_rows, slots, positions=None, release=None,
                seq_lens_out=None, free_count_out=None, stream=None):
@@ -207,54 +222,54 @@ class Nibble:
             self._ints("release", release, n, True)
         self._table(block_tables, n)
         dwkv_nibble_tables(self.h, n, n_new, release, seq_lens, block_tables, free_list, free_count, lens_out, count_out,
-                           rows, cu_rows, positions, slots, _raw(stream, self.device))
+                           rows, cu_rows, positions, slots, self._stream(stream))
 
     def append(self, k, v, slots, pool, stream=None):
         """k, v: [rows][Hkv][d] (rows may be strided views); slots int32 [rows], -1 skips a row."""
-        ks, vs = self._rows("k", k, self.cfg.num_kv_heads), self._rows("v", v, self.cfg.num_kv_heads)
-        n = k.shape[0]
-        if v.shape[0] != n:
-            raise ValueError(f"k has {n} rows and v {v.shape[0]}")
+        n, ks = self._rows("k", k, self.num_kv_heads)
+        nv, vs = self._rows("v", v, self.num_kv_heads)
+        if nv != n:
+            raise ValueError(f"k has {n} rows and v {nv}")
         self._ints("slots", slots, n, True)
         self._pool(pool)
-        dwkv_nibble_append(self.h, n, k, ks, v, vs, slots, pool, _raw(stream, self.device))
+        dwkv_nibble_append(self.h, n, k, ks, v, vs, slots, pool, self._stream(stream))
 
     def read(self, slots, pool, stream=None):
         """(k, v) [rows][Hkv][d]: the stored values of the given slots."""
         n = slots.numel()
         self._ints("slots", slots, n)
         self._pool(pool)
-        k = torch.empty(n, self.cfg.num_kv_heads, self.cfg.head_dim, dtype=self.dtype, device=self.device)
+        k = torch.empty(n, self.num_kv_heads, self.head_dim, dtype=self.dtype, device=self.device)
         v = torch.empty_like(k)
-        dwkv_nibble_read(self.h, n, slots, pool, k, v, _raw(stream, self.device))
+        dwkv_nibble_read(self.h, n, slots, pool, k, v, self._stream(stream))
         return k, v
 
     def attention(self, q, cu_rows, seq_lens, block_tables, pool, max_q, out=None, lse=None, want_lse=False, stream=None):
-        """out [rows][Hq][d] (with want_lse or lse: (out, lse), lse fp32 [rows][Hq]).  A tensor that
-        is allocated here starts as zeros (lse: -inf) where q has rows that no request has."""
-        c = self.cfg
-        qs, n, rows = self._rows("q", q, c.num_q_heads), seq_lens.numel(), q.shape[0]
+        """out [rows][Hq][d] (with want_lse or lse: (out, lse), lse fp32 [rows][Hq]).  In tensors that
+        are allocated here, rows that no request has are not set."""
+        hq, d = self.num_q_heads, self.head_dim
+        (rows, qs), n = self._rows("q", q, hq), seq_lens.numel()
         self._ints("seq_lens", seq_lens, n)
         self._ints("cu_rows", cu_rows, n + 1, True)
         self._table(block_tables, n)
         self._pool(pool)
         if out is None:
-            out = torch.empty(rows, c.num_q_heads, c.head_dim, dtype=self.dtype, device=self.device)
-        elif self._rows("out", out, c.num_q_heads) != c.num_q_heads * c.head_dim or out.shape[0] != rows:
+            out = torch.empty(rows, hq, d, dtype=self.dtype, device=self.device)
+        elif self._rows("out", out, hq) != (rows, hq * d):
             raise ValueError("out must be contiguous and have q's rows")
         if lse is not None:
-            if lse.dtype != torch.float32 or lse.device != self.device or not lse.is_contiguous() or \
-                    lse.numel() != rows * c.num_q_heads:
-                raise ValueError(f"lse must be contiguous float32 [{rows}][{c.num_q_heads}] on {self.device}")
+            if lse.dtype is not torch.float32 or lse.get_device() != self.index or not lse.is_contiguous() or \
+                    lse.numel() != rows * hq:
+                raise ValueError(f"lse must be contiguous float32 [{rows}][{hq}] on {self.device}")
         elif want_lse:
-            lse = torch.empty(rows, c.num_q_heads, dtype=torch.float32, device=self.device)
+            lse = torch.empty(rows, hq, dtype=torch.float32, device=self.device)
         dwkv_nibble_attention(self.h, n, rows, int(max_q), q, qs, cu_rows, seq_lens, block_tables, pool, out, lse,
-                              _raw(stream, self.device))
+                              self._stream(stream))
         return out if lse is None else (out, lse)
 
     def sync(self, stream=None):
         """Waits for the stream and raises DwkvError if a kernel recorded an error."""
-        dwkv_nibble_sync_status(self.h, _raw(stream, self.device))
+        dwkv_nibble_sync_status(self.h, self._stream(stream))
 
 
 class NibbleCache:

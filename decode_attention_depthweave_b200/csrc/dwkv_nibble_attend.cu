@@ -67,12 +67,12 @@ cudaError_t nib_attend(const NibGeom& G, NibAttend A, int sms, uint8_t* arena, c
     const long long most = (long long)A.max_q * G.g;          // rows x heads of a request at most
     A.rows_hi = (int)std::min<long long>(most, kNdRows);
     if (most <= kNdRows) return decode_rows(G, A, A.rows_hi, sms, s, false);
-    // Requests of few rows go to the decode kernel, the others to the chunk kernel; a request alone needs
-    // one launch only.
+    // Requests of one query row go to the decode kernel (its smallest instantiation that holds them), the others
+    // to the chunk kernel; a request alone needs one launch only.
     cudaError_t e = cudaSuccess;
-    if (A.n > 1) {
+    if (A.n > 1 && G.g <= kNdRows) {
+        A.rows_lo = A.rows_hi = G.g <= 4 ? 4 : G.g <= 8 ? 8 : kNdRows;
         e = decode_rows(G, A, A.rows_hi, sms, s, false);
-        A.rows_lo = kNdRows;
     }
     return e != cudaSuccess ? e : chunk_rows(G, A, sms, s, false);
 }

@@ -58,10 +58,9 @@ struct NcLayout {
     static constexpr int kRec = 2 * kNcRows * (D + 2);                             // floats of a record
 };
 
-// Items of a request: its tokens, rows and 256-row items.
+// A request's tokens, query rows and 256-row items.
 struct NcSpan {
     int len, nq, items;
-    long long units;                                     // of one kv-head
 };
 // Item x of a request: first token and units.
 __device__ __forceinline__ void nc_item(const NibGeom& G, int len, int nq, int x, int& base, int& units) {
@@ -71,15 +70,22 @@ __device__ __forceinline__ void nc_item(const NibGeom& G, int len, int nq, int x
     units = max(1, (hi + 1 - base + kNcTokens - 1) / kNcTokens) + kNcBorder;
 }
 __device__ __forceinline__ NcSpan nc_span(const NibGeom& G, const NibAttend& A, int b) {
-    NcSpan s{0, 0, 0, 0};
+    NcSpan s{0, 0, 0};
     if (!nib_request(G, A, b, s.len, s.nq) || s.nq == 0 || s.nq * G.g <= A.rows_lo) { s.nq = 0; return s; }
     s.items = (s.nq * G.g + 2 * kNcRows - 1) / (2 * kNcRows);
-    for (int x = 0; x < s.items; ++x) {
+    return s;
+}
+// Units of one kv-head of a request; the warp's lanes share its items.
+__device__ __forceinline__ long long nc_units(const NibGeom& G, const NcSpan& s, int lane) {
+    long long sum = 0;
+    for (int x = lane; x < s.items; x += 32) {
         int base, units;
         nc_item(G, s.len, s.nq, x, base, units);
-        s.units += units;
+        sum += units;
     }
-    return s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    return sum;
 }
 
 // The walk over the segments (parts of items) of a CTA's range.
@@ -246,22 +252,17 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     long long total, at;
     int ctas;
     {
-        const int per = (A.n + kNcThreads - 1) / kNcThreads;
-        const int b0 = min(A.n, tid * per), b1 = min(A.n, b0 + per);
+        // a warp a run of requests
+        constexpr int kWarps = kNcThreads / 32;
+        const int per = (A.n + kWarps - 1) / kWarps, b0 = min(A.n, warp * per), b1 = min(A.n, b0 + per);
         long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += nc_span(G, A, b).units * G.hkv;
-        long long before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(~0u, before, o);
-            if (lane >= o) before += y;
-        }
-        if (lane == 31) s_sum[warp] = before;
-        before -= mine;
+        for (int b = b0; b < b1; ++b) mine += nc_units(G, nc_span(G, A, b), lane) * G.hkv;
+        if (lane == 0) s_sum[warp] = mine;
         __syncthreads();
+        long long before = 0;
         total = 0;
-        for (int k = 0; k < kNcThreads / 32; ++k) {
-            if (k == warp) before += total;
+        for (int k = 0; k < kWarps; ++k) {
+            if (k == warp) before = total;
             total += s_sum[k];
         }
         if (total == 0) return;
@@ -273,21 +274,36 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             long long u = at - before;
             for (int b = b0; b < b1; ++b) {
                 const NcSpan s = nc_span(G, A, b);
-                if (u < s.units * G.hkv) {
-                    s_start[0] = b;
-                    s_start[1] = (int)(u / s.units);
-                    u %= s.units;
-                    int x = 0, base, units;
-                    for (;; ++x) {
-                        nc_item(G, s.len, s.nq, x, base, units);
-                        if (u < units) break;
-                        u -= units;
+                const long long units = nc_units(G, s, lane);
+                if (u >= units * G.hkv) {
+                    u -= units * G.hkv;
+                    continue;
+                }
+                const int h = (int)(u / units);
+                u -= h * units;
+                for (int x0 = 0;; x0 += 32) {            // 32 items at a time
+                    int base, n = 0;
+                    if (x0 + lane < s.items) nc_item(G, s.len, s.nq, x0 + lane, base, n);
+                    int pre = n;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(~0u, pre, o);
+                        if (lane >= o) pre += y;
                     }
-                    s_start[2] = x;
-                    s_start[3] = (int)u;
+                    const int all = __shfl_sync(~0u, pre, 31);
+                    if (u >= all) {
+                        u -= all;
+                        continue;
+                    }
+                    if (u >= pre - n && u < pre) {
+                        s_start[0] = b;
+                        s_start[1] = h;
+                        s_start[2] = x0 + lane;
+                        s_start[3] = (int)u - (pre - n);
+                    }
                     break;
                 }
-                u -= s.units * G.hkv;
+                break;
             }
         }
         __syncthreads();

@@ -116,9 +116,19 @@ struct NcWalk {
     }
 };
 
-__device__ __forceinline__ uint64_t nc_desc(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr >> 4) & 0x3fffu) | ((uint64_t)((lbo >> 4) & 0x3fffu) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptor, 128-byte swizzle: its low word holds the address and the leading byte offset
+// (each >> 4), its high word the stride between 8-row atoms, version 1 and the layout type 2.
+constexpr uint32_t kNcDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t nc_desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3fffu) | (lbo >> 4) << 16; }
+__device__ __forceinline__ uint64_t nc_desc(uint32_t lo) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kNcDescHi));
+    return d;
+}
+__device__ __forceinline__ bool nc_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void nc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -203,7 +213,6 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     uint8_t* sm = raw_sm + (sbase - smem_addr(raw_sm));
     // barriers
     const uint32_t bars = sbase + L::kBars;
-    auto k_full = [&](int s) { return bars + 8u * s; };
     auto k_empty = [&](int s) { return bars + 16u + 8u * s; };
     auto v_full = [&](int s) { return bars + 32u + 8u * s; };
     auto v_empty = [&](int s) { return bars + 48u + 8u * s; };
@@ -232,17 +241,16 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     };
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(k_full(s), kNcBlocks);
             mbar_init(k_empty(s), 1u);
             mbar_init(v_full(s), kNcBlocks);
             mbar_init(v_empty(s), 1u);
             mbar_init(s_full(s), 1u);
-            mbar_init(p_ready(s), kNcTile);
+            mbar_init(p_ready(s), kNcTile / 32);             // an arrival a warp: 256 on one address take their turns
             mbar_init(o_full(s), 1u);
             mbar_init(raw_full(s), kNcBlocks);
             mbar_init(raw_empty(s), kNcBlocks);
         }
-        mbar_init(q_ready, kNcSoftmax);
+        mbar_init(q_ready, kNcSoftmax / 32);
         *dead = 0;
         fence_mbar_init();
     }
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
         do all_units += c.count(); while (c.next(G, A));
     }
 
-    if (warp == kNcSoftmax / 32 + 1) {
+    if (warp == 1) {
         // ================= loader: lane x copies the keys' half of block x of unit n, lane 8 + x the values' half of
         // unit n - 1, each with a walk of its own
         if (lane < 2 * kNcBlocks) {
@@ -375,70 +383,89 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             if (!ok) mbar_wait_for(full, 0u, 10000000ull), mbar_wait_for(full, 1u, 10000000ull);   // what is in flight, within a limit
         }
         __syncwarp();
-    } else if (warp == kNcSoftmax / 32) {
-        // ================= MMA: one thread
-        if (lane == 0) {
-            bool ok = true, any = false;
-            uint32_t j = 0, items = 0, done[2] = {0, 0};  // units; segments; units of each tile
-            // S of unit jj; O += P V of it (start: O starts)
-            auto qk = [&](int t, uint32_t jj) {
-                const uint32_t qb = sbase + L::kQ + t * L::kTile, kb = sbase + L::kK + (jj & 1) * L::kTile;
+    } else if (warp == 0) {
+        // ================= MMA: the warp walks and waits together, one elected lane issues, so that addresses
+        // and descriptors stay in uniform registers
+        bool ok = true, any = false;
+        uint32_t j = 0, items = 0, done0 = 0, done1 = 0;  // units; segments; units of each tile
+        uint32_t q_lo[2], k_lo[2], v_lo[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            q_lo[x] = nc_desc_lo(sbase + L::kQ + x * L::kTile, 16u);
+            k_lo[x] = nc_desc_lo(sbase + L::kK + x * L::kTile, 16u);
+            v_lo[x] = nc_desc_lo(sbase + L::kV + x * L::kTile, L::kHalf);
+        }
+        // S of unit jj; O += P V of it (start: O starts)
+        auto qk = [&](int t, uint32_t jj) {
+            const uint32_t a = t ? q_lo[1] : q_lo[0], b = jj & 1 ? k_lo[1] : k_lo[0], d = tmem + kTmS + t * 128, bar = s_full(t);
+            if (nc_elect()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * L::kHalf + (k & 3) * 32u;
-                    nc_mma_ss(tmem + kTmS + t * 128, nc_desc(qb + off, 16u), nc_desc(kb + off, 16u), kIdescS, k ? 1u : 0u);
+                    const uint32_t off = ((k >> 2) * L::kHalf + (k & 3) * 32u) >> 4;
+                    nc_mma_ss(d, nc_desc(a + off), nc_desc(b + off), kIdescS, k ? 1u : 0u);
                 }
-                nc_commit(s_full(t));
-                any = true;
-            };
-            auto pv = [&](int t, uint32_t jj, bool start) {
-                const uint32_t vb = sbase + L::kV + (jj & 1) * L::kTile;
+                nc_commit(bar);
+            }
+            __syncwarp();
+            any = true;
+        };
+        auto pv = [&](int t, uint32_t jj, bool start) {
+            const uint32_t b = jj & 1 ? v_lo[1] : v_lo[0], d = tmem + kTmO + t * D, p = tmem + kTmS + t * 128;
+            if (nc_elect()) {
 #pragma unroll
                 for (int k = 0; k < kNcTokens / 16; ++k)
-                    nc_mma_ts(tmem + kTmO + t * D, tmem + kTmS + t * 128 + (k >> 2) * 64 + 8 * (k & 3), nc_desc(vb + k * 2048u, L::kHalf), kIdescO,
-                              start && k == 0 ? 0u : 1u);
-            };
-            auto after = [&](bool got) {
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                return got;
-            };
-            for (bool some = true; ok && some; some = w.next(G, A), ++items) {
-                const int cnt = w.count(), tiles = w.s.nq * G.g - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
-                ok = after(wait(q_ready, items & 1u) && wait(k_full(j & 1), (j >> 1) & 1u));
-                if (!ok) break;
-                for (int t = 0; t < tiles; ++t) qk(t, j);
-                nc_commit(k_empty(j & 1));
-                for (int u = 0; ok && u < cnt; ++u, ++j) {
-                    for (int t = 0; ok && t < tiles; ++t) {
-                        ok = wait(p_ready(t), done[t] & 1u);
-                        ++done[t];
-                        if (ok && t == 0) ok = wait(v_full(j & 1), (j >> 1) & 1u);
-                        if (!after(ok)) break;
-                        pv(t, j, u == 0);
-                        if (u + 1 == cnt) {
-                            nc_commit(o_full(t));
-                        } else {
-                            if (t == 0) ok = after(wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1u));
-                            if (ok) qk(t, j + 1);
-                        }
+                    nc_mma_ts(d, p + (k >> 2) * 64 + 8 * (k & 3), nc_desc(b + k * (2048u >> 4)), kIdescO, start && k == 0 ? 0u : 1u);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint32_t bar) {
+            if (nc_elect()) nc_commit(bar);
+            __syncwarp();
+        };
+        auto after = [&](bool got) {
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            return got;
+        };
+        for (bool some = true; ok && some; some = w.next(G, A), ++items) {
+            const int cnt = w.count(), tiles = w.s.nq * G.g - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
+            ok = __all_sync(~0u, wait(q_ready, items & 1u));   // tile 0's warps wrote the first unit's keys before
+            if (!after(ok)) break;
+            qk(0, j);
+            if (tiles > 1) qk(1, j);
+            commit(k_empty(j & 1));
+            for (int u = 0; ok && u < cnt; ++u, ++j) {
+                // a tile's weights are there: its values' product, and the next unit's scores
+                auto turn = [&](int t, uint32_t& done) {
+                    if (t == 0) ok = wait(v_full(j & 1), (j >> 1) & 1u);
+                    ok = __all_sync(~0u, ok && wait(p_ready(t), done & 1u));
+                    ++done;
+                    if (!after(ok)) return;
+                    pv(t, j, u == 0);
+                    if (u + 1 == cnt) {
+                        commit(o_full(t));
+                    } else {
+                        qk(t, j + 1);                    // its keys are there: tile 0's warps wrote them before these weights
                     }
-                    if (!ok) break;
-                    nc_commit(v_empty(j & 1));
-                    if (u + 1 < cnt) nc_commit(k_empty((j + 1) & 1));
-                }
+                };
+                turn(0, done0);
+                if (ok && tiles > 1) turn(1, done1);
+                if (!ok) break;
+                commit(v_empty(j & 1));
+                if (u + 1 < cnt) commit(k_empty((j + 1) & 1));
             }
-            if (!ok && any) {                            // the products in flight end first, within a limit
-                nc_commit(s_full(0));
-                mbar_wait_for(s_full(0), j & 1u, 10000000ull);
-            }
+        }
+        if (!ok && any) {                                // the products in flight end first, within a limit
+            commit(s_full(0));
+            mbar_wait_for(s_full(0), j & 1u, 10000000ull);
         }
         __syncwarp();
     } else {
         // ================= softmax: a thread a row of tile t
         // A wait that ran out leaves ok false: the loops run to their end without waiting or issuing, so
         // that every thread meets the others at the barriers.
-        const int t = warp >> 3, hc = (warp >> 2) & 1, r = tid & (kNcRows - 1);   // tile, its tokens' (and O's channels') half, row
-        const bool leader = (tid & (kNcTile - 1)) == 0;
+        const int sw = warp - 2, t = sw >> 3, hc = (sw >> 2) & 1;    // tile, its tokens' (and O's channels') half
+        const int r = (warp & 3) * 32 + lane;                        // row: a warp reaches the tensor-memory lanes of its number mod 4
+        const bool leader = (sw & 7) == 0 && lane == 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // this warp's tensor-memory lanes (32 of 128, bits 16 up)
         const uint32_t s_at = tmem + lanes + kTmS + t * 128 + hc * 64, o_at = tmem + lanes + kTmO + t * D + hc * (D / 2);
         float* ex = reinterpret_cast<float*>(sm + L::kEx) + t * 2 * kNcRows;       // [2][2 tiles][2 halves][rows]
@@ -449,7 +476,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
         // token are not to be believed.  Eight lanes take one 32-channel chunk of eight tokens: all stores, and the
         // loads of values, fall in distinct banks.  All loads come before the first store, which the compiler could
         // not know to be elsewhere.
-        const int blk_of = warp & (kNcBlocks - 1);
+        const int blk_of = sw & (kNcBlocks - 1);
         auto unpack_as = [&](auto zz, uint32_t n) {
             constexpr int z = decltype(zz)::value;
             if (n >= (uint32_t)all_units) return;
@@ -490,7 +517,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             __syncwarp();
             if (lane == 0 && ok) {
                 mbar_arrive(raw_empty(z));
-                mbar_arrive(z ? v_full(n & 1) : k_full(n & 1));
+                if (z) mbar_arrive(v_full(n & 1));       // keys: the weights or queries that follow say it
             }
         };
         // what the tile's warps prepare after unit n: keys two units ahead, or values one
@@ -504,7 +531,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             const int cnt = w.count(), rows = w.s.nq * G.g, row = 2 * kNcRows * w.x + kNcRows * t + r;
             const int tiles = rows - 2 * kNcRows * w.x > kNcRows ? 2 : 1;
             if (t >= tiles) {                            // no such tile; the queries' barrier counts all the same
-                mbar_arrive(q_ready);
+                if (lane == 0) mbar_arrive(q_ready);
                 for (int u = 0; u < cnt; ++u, ++units) {
                     unpack(units);
                 }
@@ -517,42 +544,50 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             const int row0 = A.cu[w.b];
             const bool have = row < rows;
             const int jq = have ? row / G.g : 0, hg = have ? row - jq * G.g : 0;
-            // ---- the query row, scaled by a power of two to below 2, as fp16
-            float fac = 1.f;
+            // ---- the query row, scaled by a power of two to below 2, as fp16; half a row a thread
+            float fac;
             {
-                const uint16_t* qp = A.q + (size_t)(row0 + jq) * A.q_stride + (size_t)(w.h * G.g + hg) * D;
+                const uint16_t* qp = A.q + (size_t)(row0 + jq) * A.q_stride + (size_t)(w.h * G.g + hg) * D + hc * (D / 2);
+                uint4 v[D / 16];
                 float a = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = have ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) v[c] = have ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         a = fmaxf(a, fabsf(FP16 ? half_lo(x[y]) : bf16lo(x[y])));
                         a = fmaxf(a, fabsf(FP16 ? half_hi(x[y]) : bf16hi(x[y])));
                     }
                 }
+                float* place = ex + (~units & 1u) * 4 * kNcRows;         // not where the last segment left its sums
+                place[hc * kNcRows + r] = a;
+                named_barrier(1 + t, kNcTile);
+                a = fmaxf(a, place[(hc ^ 1) * kNcRows + r]);
                 const uint32_t e = min(max(__float_as_uint(a) >> 23, 1u), 253u);
                 const float sc = __uint_as_float((254u - e) << 23);
+                // not 0, however small the scale: a masked score is -inf times it
                 fac = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
                 uint8_t* dst = sm + L::kQ + t * L::kTile + r * 128;
-#pragma unroll 4
-                for (int c = hc * (D / 16); c < (hc + 1) * (D / 16); ++c) {          // half the row a thread
-                    const uint4 v = have ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                    const int c8 = hc * (D / 16) + c;
                     float f[8];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         f[2 * y] = (FP16 ? half_lo(x[y]) : bf16lo(x[y])) * sc;
                         f[2 * y + 1] = (FP16 ? half_hi(x[y]) : bf16hi(x[y])) * sc;
                     }
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kHalf + (((c & 7) ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(dst + (c8 >> 3) * L::kHalf + (((c8 & 7) ^ (r & 7)) << 4)) =
                         make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
                 }
                 fence_async_smem();
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            mbar_arrive(q_ready);                        // the tile's queries are there, its O is read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);         // the tile's queries are there, its O is read
             ++segs;
             const int hi = have ? w.s.len - w.s.nq + jq : -1;        // last token the row sees
             // the tile's rows see all of a unit within [all_lo, all_hi]
@@ -590,26 +625,39 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                         for (int y = 0; y < 32; ++y) x[y] = (seen[c] >> y) & 1u ? x[y] : -INFINITY;
                     }
                 };
-                float top = -INFINITY;
+                uint32_t pk[32];
+                float sum, top;
+                for (bool again = false;;) {             // a second time when the maximum moves
+                    const float2 c0 = make_float2(kNdBias - m, kNdBias - m), f2 = make_float2(fac, fac);
+                    float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x[32];
-                    nc_ld32(s_at + 32 * c, x);
-                    mask(x, c);
-                    float tops[4] = {x[0], x[1], x[2], x[3]};
+                    for (int c = 0; c < 2; ++c) {
+                        float x[32];
+                        nc_ld32(s_at + 32 * c, x);
+                        mask(x, c);
+                        float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int y = 4; y < 32; y += 4)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) tops[z] = fmaxf(tops[z], x[y + z]);
-                    top = fmaxf(top, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
-                }
-                // the row's other half; two places in turn, so that one barrier a unit will do
-                float* place = ex + (units & 1u) * 4 * kNcRows;
-                place[hc * kNcRows + r] = top;
-                named_barrier(1 + t, kNcTile);
-                top = fmaxf(top, place[(hc ^ 1) * kNcRows + r]);
-                const float mx = top > -INFINITY ? top * fac : kNdNone;
-                if (__any_sync(~0u, mx > m + kNdLag)) {
+                        for (int y = 0; y < 32; y += 2) {
+                            tops[(y >> 1) & 1] = fmaxf(tops[(y >> 1) & 1], fmaxf(x[y], x[y + 1]));
+                            const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
+                            const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                            sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
+                            pk[16 * c + y / 2] = pack_half2(p.x, p.y);
+                        }
+                        top = fmaxf(top, fmaxf(tops[0], tops[1]));
+                    }
+                    const float2 sa = add2(sums[0], sums[1]);
+                    sum = sa.x + sa.y;
+                    if (again) break;
+                    // the row's maximum over both halves; two places in turn, so that one barrier a unit will do
+                    float* place = ex + (units & 1u) * 4 * kNcRows;
+                    place[hc * kNcRows + r] = top;
+                    named_barrier(1 + t, kNcTile);
+                    top = fmaxf(top, place[(hc ^ 1) * kNcRows + r]);
+                    const float mx = top > -INFINITY ? top * fac : kNdNone;
+                    if (!__any_sync(~0u, mx > m + kNdLag)) break;
+                    again = true;
                     const float mn = fmaxf(m, mx), f = ex2(m - mn);
                     m = mn;
                     l *= f;
@@ -625,28 +673,12 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                         }
                     }
                 }
-                const float2 c0 = make_float2(kNdBias - m, kNdBias - m), f2 = make_float2(fac, fac);
-                float2 sums[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x[32];
-                    nc_ld32(s_at + 32 * c, x);
-                    mask(x, c);
-#pragma unroll
-                    for (int y = 0; y < 32; y += 2) {
-                        const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
-                        const float2 p = make_float2(ex2(z.x), ex2(z.y));
-                        sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
-                        pk[16 * c + y / 2] = pack_half2(p.x, p.y);
-                    }
-                }
-                const float2 sa = add2(sums[0], sums[1]);
-                l = sa.x + sa.y;
+                l += sum;
                 nc_st32(s_at, pk);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                mbar_arrive(p_ready(t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready(t));
                 unpack(units);
             }
             // ---- the segment ends

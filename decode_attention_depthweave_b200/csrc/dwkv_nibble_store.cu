@@ -18,7 +18,8 @@ namespace dwkv {
 // costs no more than many short ones.  The only dependency is pops and in-place updates after
 // pushes and reads: one cluster barrier.
 // ------------------------------------------------------------------------------------
-constexpr int kTabThreads = 1024;
+constexpr int kTabThreads = 1024;                 // at most
+constexpr int kTabRows = 4;                       // rows in flight a thread
 constexpr int kRowCap = 1 << 30;                 // the prefix sums saturate here
 
 __device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kRowCap); }
@@ -37,7 +38,7 @@ static size_t nib_tables_smem(int n) { return (size_t)(5 * (n + 1) + 3 * 32) * 4
 
 __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G, const NibTables T) {
     extern __shared__ int tsm[];
-    const int n = T.n, P = G.page;
+    const int n = T.n, P = G.page, sh = G.page_shift, threads = blockDim.x;
     int* back = tsm;                             // [n + 1] exclusive prefix sums
     int* need = back + n + 1;
     int* rows = need + n + 1;
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
     const long long most = (long long)G.max_blocks * P;
-    const int per = (n + kTabThreads - 1) / kTabThreads;
+    const int per = (n + threads - 1) / threads;
     const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
     int sb = 0, sn = 0, sr = 0;
     for (int b = b0; b < b1; ++b) {
@@ -61,12 +62,12 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
             nw = 0;
             if (rank == 0) nib_error(G, 10u /*DWKV_DEV_BAD_LENGTH*/, (uint32_t)b, (uint32_t)len);
         } else {
-            if (rel) { bk = (len + P - 1) / P; len = 0; }
+            if (rel) { bk = (len + P - 1) >> sh; len = 0; }
             if ((long long)len + nw > most) {
                 f |= 4;                          // longer than a table row: refused, its rows still count
                 if (rank == 0) nib_error(G, 10u, (uint32_t)b, (uint32_t)nw);
             } else {
-                nd = (len + nw + P - 1) / P - (len + P - 1) / P;
+                nd = ((len + nw + P - 1) >> sh) - ((len + P - 1) >> sh);
             }
         }
         now[b] = len;
@@ -88,7 +89,8 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
     if (lane == 31) { red[warp] = pb; red[32 + warp] = pn; red[64 + warp] = pr; }
     __syncthreads();
     if (warp == 0) {
-        int x = red[lane], y = red[32 + lane], z = red[64 + lane];
+        const bool in = lane < threads / 32;
+        int x = in ? red[lane] : 0, y = in ? red[32 + lane] : 0, z = in ? red[64 + lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(~0u, x, o), v = __shfl_up_sync(~0u, y, o), w = __shfl_up_sync(~0u, z, o);
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
     const int top = min(count + all_back, G.num_pages);
     if (rank == 0 && tid == 0 && count + all_back > G.num_pages) nib_error(G, 7u /*DWKV_DEV_FREE_LIST*/, (uint32_t)count, (uint32_t)all_back);
     // served: its pages fit and its rows have a place
-    for (int b = tid; b < n; b += kTabThreads) {
+    for (int b = tid; b < n; b += threads) {
         const int nd = need[b + 1] - need[b];
         int f = ok[b];
         if (!(f & 4)) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
         }
         ok[b] = f;
     }
-    const int gt = (int)rank * kTabThreads + tid, gn = (int)ncta * kTabThreads;
+    const int gt = (int)rank * threads + tid, gn = (int)ncta * threads;
     // push
     for (int i = gt; i < all_back && count + i < G.num_pages; i += gn) {
         const int b = find_in(back, n, i);
@@ -144,26 +146,34 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
     const int all_need = min(need[n], top);
     for (int i = gt; i < all_need; i += gn) {
         const int b = find_in(need, n, i);
-        if (ok[b] & 1) T.table[(size_t)b * G.max_blocks + (now[b] + P - 1) / P + (i - need[b])] = T.free_list[top - 1 - i];
+        if (ok[b] & 1) T.table[(size_t)b * G.max_blocks + ((now[b] + P - 1) >> sh) + (i - need[b])] = T.free_list[top - 1 - i];
     }
-    // rows
-    for (int r = gt; r < T.max_rows; r += gn) {
-        int pos = -1, slot = -1;
-        if (r < rows[n]) {
-            const int b = find_in(rows, n, r);
-            if (ok[b] & 1) {
-                pos = now[b] + r - rows[b];
-                const int had = (now[b] + P - 1) / P, j = pos / P;
-                const int id = j < had ? T.table[(size_t)b * G.max_blocks + j] : T.free_list[top - 1 - (need[b] + j - had)];
-                slot = id * P + pos % P;
-                if ((unsigned)id >= (unsigned)G.num_pages) {
-                    nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)b, (uint32_t)id);
-                    slot = -1;
+    // rows, kTabRows in flight a thread: their requests, then their pages, then the stores
+    const int all_rows = min(rows[n], T.max_rows);
+    for (int r0 = gt; r0 < T.max_rows; r0 += gn * kTabRows) {
+        int pos[kTabRows], id[kTabRows];
+#pragma unroll
+        for (int k = 0; k < kTabRows; ++k) {
+            const int r = r0 + k * gn;
+            pos[k] = id[k] = -1;
+            if (r < all_rows) {
+                const int b = find_in(rows, n, r);
+                if (ok[b] & 1) {
+                    const int at = now[b] + r - rows[b], had = (now[b] + P - 1) >> sh, j = at >> sh;
+                    pos[k] = at;
+                    id[k] = j < had ? T.table[(size_t)b * G.max_blocks + j] : T.free_list[top - 1 - (need[b] + j - had)];
                 }
             }
         }
-        T.slots[r] = slot;
-        if (T.positions) T.positions[r] = pos;
+#pragma unroll
+        for (int k = 0; k < kTabRows; ++k) {
+            const int r = r0 + k * gn;
+            if (r >= T.max_rows) break;
+            const bool good = (unsigned)id[k] < (unsigned)G.num_pages;
+            if (pos[k] >= 0 && !good) nib_error(G, 11u /*DWKV_DEV_BAD_PAGE*/, (uint32_t)r, (uint32_t)id[k]);
+            T.slots[r] = good ? (id[k] << sh) + (pos[k] & (P - 1)) : -1;
+            if (T.positions) T.positions[r] = pos[k];
+        }
     }
     if (rank == 0) {
         int taken = 0;
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
         __syncthreads();
         if (tid == 0) {
             int s = 0;
-            for (int w = 0; w < kTabThreads / 32; ++w) s += red[w];
+            for (int w = 0; w < threads / 32; ++w) s += red[w];
             *T.count_out = top - s;
             T.cu_rows[n] = rows[n];
         }
@@ -228,6 +238,20 @@ __device__ __forceinline__ bool nib_row(const NibGeom& G, const NibRows& R, NibR
     return true;
 }
 
+template <bool FP16>
+__device__ __forceinline__ float lo16(uint32_t w) {
+    return FP16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))) : bf16lo(w);
+}
+template <bool FP16>
+__device__ __forceinline__ float hi16(uint32_t w) { return FP16 ? __half2float(__ushort_as_half((unsigned short)(w >> 16))) : bf16hi(w); }
+template <bool FP16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (FP16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 template <int D, bool FP16>
 __global__ void __launch_bounds__(32 * kRowWarps) nib_append_kernel(const NibGeom G, const NibRows R) {
     constexpr int LV = D / 8, HS = 32 / LV;                       // lanes of a vector, heads side by side
@@ -247,18 +271,18 @@ __global__ void __launch_bounds__(32 * kRowWarps) nib_append_kernel(const NibGeo
         for (int k = 0; k < kAhead; ++k) {
             const int h = h0 + k * HS;
             const uint32_t ws[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
-            float f[8], a = 0.f;
+            // the largest magnitude, two 16-bit values at a time; a NaN makes it NaN
+            const uint32_t top2 = max2<FP16>(max2<FP16>(ws[0] & 0x7fff7fffu, ws[1] & 0x7fff7fffu),
+                                             max2<FP16>(ws[2] & 0x7fff7fffu, ws[3] & 0x7fff7fffu));
+            float f[8], a = fmaxf(lo16<FP16>(top2), hi16<FP16>(top2));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t b = (ws[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-                f[j] = FP16 ? __half2float(__ushort_as_half((unsigned short)b)) : __uint_as_float(b << 16);
-                a = fmaxf(a, fabsf(f[j]));
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] = lo16<FP16>(ws[j]);
+                f[2 * j + 1] = hi16<FP16>(ws[j]);
             }
-            // NaN, infinite or beyond the largest value (rare): NaN to 0, the rest clamped
-            bool odd = a > 7.f * kNibScaleMax;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) odd |= f[j] != f[j];
-            if (odd) {
+            // NaN, infinite or beyond the largest value (rare): NaN to 0, the rest clamped.  (fmaxf leaves a NaN
+            // out: one in either half shows in the other test.)
+            if (!(lo16<FP16>(top2) <= 7.f * kNibScaleMax) || !(hi16<FP16>(top2) <= 7.f * kNibScaleMax)) {
                 a = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -272,17 +296,23 @@ __global__ void __launch_bounds__(32 * kRowWarps) nib_append_kernel(const NibGeo
             if (h >= G.hkv) continue;
             const uint32_t sb = e5m3_of(__fdiv_rn(a, 7.f));
             const float s = nib_scale((uint8_t)sb), r = sb ? __frcp_rn(s) : 0.f;
-            uint32_t u = 0;
+            // q = f / s rounded once: a product with 1/s and one step by its exact remainder.  At a tie of the codes q
+            // is exact, and elsewhere far from one, so that the sum with 1.5 2^23 rounds it as the definition does
+            // (ties to even).  All on the floating-point pipe: the integer one bound this kernel (40 us at 16384 rows).
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                // rint(f / s), ties to even, without a division: n is the nearest whole number to f (1/s) (two
-                // roundings, so it may be either one at a tie), e = f - n s is exact, and |e| = s / 2 is a tie
-                float n = rintf(f[j] * r);
-                const float e = fmaf(-n, s, f[j]);
-                if (fabsf(e) == 0.5f * s && (__float2int_rn(n) & 1)) n += copysignf(1.f, e);
-                const int c = max(-7, min(7, __float2int_rn(n)));
-                u |= (uint32_t)(c + 8) << (4 * j);
+                float q = f[j] * r;
+                q = fmaf(fmaf(-q, s, f[j]), r, q);
+                f[j] = (q + 12582912.f) - 12582912.f;
             }
+            if (sb < 8) {                                         // below 2^-14 s is coarse and the codes may pass 7
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = fminf(fmaxf(f[j], -7.f), 7.f);
+            }
+            // a unit is a whole number below 2^16: the mantissa of its sum with 2^23
+            const float u0 = fmaf(f[3], 4096.f, fmaf(f[2], 256.f, fmaf(f[1], 16.f, f[0] + (8388608.f + 34952.f))));
+            const float u1 = fmaf(f[7], 4096.f, fmaf(f[6], 256.f, fmaf(f[5], 16.f, f[4] + (8388608.f + 34952.f))));
+            uint32_t u = __byte_perm(__float_as_uint(u0), __float_as_uint(u1), 0x5410);
             // each 16-bit unit rotated left by 2
             u = ((u << 2) & 0xfffcfffcu) | ((u >> 14) & 0x00030003u);
             uint8_t* blk = x.base + h * head_bytes;
@@ -338,10 +368,13 @@ cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s) {
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = (T.n > 1024 || T.max_rows > 2048) ? 8 : 1;
+    // a small step is bound by barriers and loads in a row: few warps; a large one by its rows and pages
+    const bool large = T.n > 1024 || T.max_rows > 4096;
+    const int threads = T.n <= 128 && T.max_rows <= 1024 ? 128 : kTabThreads;
+    a.val.clusterDim.x = large ? 8 : 1;
     a.val.clusterDim.y = a.val.clusterDim.z = 1;
     c.gridDim = dim3(a.val.clusterDim.x);
-    c.blockDim = dim3(kTabThreads);
+    c.blockDim = dim3(threads);
     c.dynamicSmemBytes = nib_tables_smem(T.n);
     c.stream = s;
     c.attrs = &a;

@@ -102,7 +102,11 @@ cudaError_t nib_prepare_store();
 cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s);
 cudaError_t nib_append(const NibGeom& G, const NibRows& R, cudaStream_t s);
 cudaError_t nib_read(const NibGeom& G, const NibRows& R, cudaStream_t s);
-// Bytes of the handle's arena behind its first 256 (the error word): tickets, records.
+// The handle's arena: 256 bytes (the error word), the tickets, the records.  kNibMaxSms: CTAs of a launch
+// at two an SM need a ticket each, the chunk kernel's one an SM two.
+constexpr int kNibMaxSms = 160;
+constexpr size_t kNibTickets = 256, kNibRecords = kNibTickets + (size_t)2 * kNibMaxSms * 4;
+// Bytes of the records.
 size_t nib_attend_bytes(int d);
 cudaError_t nib_prepare_attend(const NibGeom& G);
 cudaError_t nib_attend(const NibGeom& G, NibAttend A, int sms, uint8_t* arena, cudaStream_t s);
@@ -140,7 +144,7 @@ __device__ __forceinline__ void nib_put(const NibGeom& G, const NibAttend& A, in
                                         float ll, float4 o) {
     const int j = r / G.g;
     const size_t at = (size_t)(row0 + j) * G.hq + (size_t)(h * G.g + r - j * G.g);
-    const float inv = ll > 0.f ? 32.f / ll : 0.f;
+    const float inv = ll == 0.f ? 0.f : 32.f / ll;            // a NaN (of the queries) stays one
     uint32_t lo, hi;
     if (FP16) {
         const __half2 a = __floats2half2_rn(o.x * inv, o.y * inv), b = __floats2half2_rn(o.z * inv, o.w * inv);
@@ -152,7 +156,7 @@ __device__ __forceinline__ void nib_put(const NibGeom& G, const NibAttend& A, in
         hi = *reinterpret_cast<const uint32_t*>(&b);
     }
     *reinterpret_cast<uint2*>(A.out + at * d + ch) = make_uint2(lo, hi);
-    if (A.lse && ch == 0) A.lse[at] = ll > 0.f ? (mm - 7.f + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    if (A.lse && ch == 0) A.lse[at] = ll == 0.f ? -INFINITY : (mm - 7.f + log2f(ll)) * 0.6931471805599453f;
 }
 
 __device__ __forceinline__ float nib_scale(uint8_t b) { return __half2float(__ushort_as_half((unsigned short)(b << 7))); }

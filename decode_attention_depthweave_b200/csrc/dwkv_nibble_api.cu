@@ -128,8 +128,7 @@ dwkv_status check_rows(const NibGeom& G, int32_t n, const void* k, int64_t ks, c
     return DWKV_OK;
 }
 
-// The error word, then the attention's tickets and records.
-size_t arena_need(const dwkv_nibble_config* c) { return 256 + nib_attend_bytes(c->head_dim); }
+size_t arena_need(const dwkv_nibble_config* c) { return kNibRecords + nib_attend_bytes(c->head_dim); }
 
 }  // namespace
 
@@ -281,7 +280,7 @@ dwkv_status dwkv_nibble_sync_status(dwkv_nibble_handle h, void* stream) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "read device error word");
     if (w[0] == 0) return DWKV_OK;
-    e = cudaMemsetAsync(h->geom.err, 0, sizeof(w), s);
+    e = cudaMemsetAsync(h->arena, 0, kNibRecords, s);              // the tickets too: a wait that ran out leaves some taken
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "clear device error word");
     const char* nm = "unknown";

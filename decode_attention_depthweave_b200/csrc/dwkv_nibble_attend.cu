@@ -7,21 +7,20 @@
 namespace dwkv {
 
 // ------------------------------------------------------------------------------ launches
-constexpr int kNdRows = 16;                                   // rows x heads that the decode kernels take
-constexpr int kMaxSms = 160;
-
-static constexpr size_t kTicketBytes = (size_t)2 * kMaxSms * 4;
-
+// Rows x heads a request that the decode kernels take.  24 requests of 12000 tokens, d 128, 8 kv-heads:
+// 4 and 8 rows 91 us, 16 rows 125, 32 rows 250; the chunk kernel, which does 128 rows' work for one, takes
+// 300 to 315 from 1 row to 128, and 380 for 256.  One request of 16384: 32 rows 49 us, in the chunk kernel 58.
+constexpr int kNdRows = 32;
 // The chunk kernel's records, two of 256 rows a CTA, are the larger ones; the launches of a call run
 // one after the other and share them.
-size_t nib_attend_bytes(int d) { return kTicketBytes + (size_t)2 * kMaxSms * 2 * kNcRows * (d + 2) * 4; }
+size_t nib_attend_bytes(int d) { return (size_t)2 * kNibMaxSms * 2 * kNcRows * (d + 2) * 4; }
 
 template <int D, int R, bool FP16>
 static cudaError_t decode_launch(const NibGeom& G, const NibAttend& A, int sms, cudaStream_t s, bool prepare) {
     using L = NdLayout<D, R>;
     auto k = nib_decode_kernel<D, R, R == 4 && FP16, FP16>;
     if (prepare) return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
-    k<<<std::min(sms, kMaxSms) * L::kCtas, kNdThreads + 32, L::kBytes, s>>>(G, A);
+    k<<<std::min(sms, kNibMaxSms) * L::kCtas, kNdThreads + 32, L::kBytes, s>>>(G, A);
     return cudaGetLastError();
 }
 
@@ -30,7 +29,8 @@ static cudaError_t decode_rows(const NibGeom& G, const NibAttend& A, int rows, i
 #define NIB_PICK(D, F)                                                                          \
     return rows <= 4 ? decode_launch<D, 4, F>(G, A, sms, s, prepare)                      \
          : rows <= 8 ? decode_launch<D, 8, F>(G, A, sms, s, prepare)                     \
-                     : decode_launch<D, 16, F>(G, A, sms, s, prepare)
+         : rows <= 16 ? decode_launch<D, 16, F>(G, A, sms, s, prepare)                   \
+                      : decode_launch<D, 32, F>(G, A, sms, s, prepare)
     if (G.d == 128) {
         if (G.fp16) NIB_PICK(128, true);
         NIB_PICK(128, false);
@@ -45,7 +45,7 @@ static cudaError_t chunk_launch(const NibGeom& G, const NibAttend& A, int sms, c
     using L = NcLayout<D>;
     auto k = nib_chunk_kernel<D, FP16>;
     if (prepare) return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
-    k<<<std::min(sms, kMaxSms), kNcThreads, L::kBytes, s>>>(G, A);
+    k<<<std::min(sms, kNibMaxSms), kNcThreads, L::kBytes, s>>>(G, A);
     return cudaGetLastError();
 }
 
@@ -56,22 +56,22 @@ static cudaError_t chunk_rows(const NibGeom& G, const NibAttend& A, int sms, cud
 
 cudaError_t nib_prepare_attend(const NibGeom& G) {
     cudaError_t e = chunk_rows(G, NibAttend{}, 0, nullptr, true);
-    for (int rows : {4, 8, 16})
+    for (int rows : {4, 8, 16, 32})
         if (e == cudaSuccess) e = decode_rows(G, NibAttend{}, rows, 0, nullptr, true);
     return e;
 }
 
 cudaError_t nib_attend(const NibGeom& G, NibAttend A, int sms, uint8_t* arena, cudaStream_t s) {
-    A.tickets = reinterpret_cast<int*>(arena + 256);
-    A.records = reinterpret_cast<float*>(arena + 256 + kTicketBytes);
+    A.tickets = reinterpret_cast<int*>(arena + kNibTickets);
+    A.records = reinterpret_cast<float*>(arena + kNibRecords);
     const long long most = (long long)A.max_q * G.g;          // rows x heads of a request at most
     A.rows_hi = (int)std::min<long long>(most, kNdRows);
     if (most <= kNdRows) return decode_rows(G, A, A.rows_hi, sms, s, false);
-    // Requests of one query row go to the decode kernel (its smallest instantiation that holds them), the others
-    // to the chunk kernel; a request alone needs one launch only.
+    // Of a batch with longer requests, those of one query row (and what else fits that instantiation) go to the
+    // decode kernel, the others to the chunk kernel; a request alone needs one launch only.
     cudaError_t e = cudaSuccess;
     if (A.n > 1 && G.g <= kNdRows) {
-        A.rows_lo = A.rows_hi = G.g <= 4 ? 4 : G.g <= 8 ? 8 : kNdRows;
+        A.rows_lo = A.rows_hi = G.g <= 4 ? 4 : G.g <= 8 ? 8 : G.g <= 16 ? 16 : kNdRows;
         e = decode_rows(G, A, A.rows_hi, sms, s, false);
     }
     return e != cudaSuccess ? e : chunk_rows(G, A, sms, s, false);

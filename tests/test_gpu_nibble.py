@@ -290,6 +290,70 @@ def test_attention(hq, hkv, d, page, dtype, window, lens, qs):
     r.check(out, lse)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hq,hkv,d,page,window,lens,qs", [
+    (17, 1, 128, 64, 0, [300], [1]),
+    (64, 2, 128, 16, 0, [777, 31, 0, 1, 448], [1, 1, 0, 1, 1]),
+    (8, 2, 128, 32, 90, [500, 225, 224, 5], [8, 5, 7, 6]),
+    (20, 1, 64, 64, 0, [2000, 449], [1, 1]),
+    (32, 1, 64, 16, 40, [333, 90], [1, 1]),
+    (6, 2, 64, 128, 0, [700, 3], [10, 9]),
+    (32, 1, 128, 64, 0, [600, 90, 450], [1, 20, 1]),
+])
+def test_attention_of_17_to_32_rows_a_kv_head(hq, hkv, d, page, window, lens, qs, dtype):
+    r = Requests(sum(lens), hq, hkv, d, page, dtype, lens, qs, window)
+    out, lse = r.run()
+    r.nb.sync()
+    r.check(out, lse)
+
+
+@pytest.mark.parametrize("longest", [1, 6, 40])
+@pytest.mark.parametrize("n", [33, 300])
+def test_attention_over_many_requests(n, longest):
+    """More requests than a warp has lanes, and than a block has threads; some idle."""
+    rng = np.random.default_rng(n + longest)
+    lens = rng.integers(0, 400, n).tolist()
+    qs = [0 if rng.random() < 0.2 else 1 if rng.random() < 0.7 else int(rng.integers(1, longest + 1)) for _ in range(n)]
+    r = Requests(n, 4, 1, 64, 16, BF, lens, qs)
+    out, lse = r.run(max_q=longest)
+    r.nb.sync()
+    r.check(out, lse)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("qs", [[1, 1], [4, 3], [8, 5], [60, 33]])
+def test_a_query_that_is_no_number_spoils_its_own_row_only(qs, bad):
+    r = Requests(41, 8, 2, 128, 64, BF, [100, 300], qs)
+    clean, clean_lse = r.run()
+    spoilt = r.q.clone()
+    spoilt[0, 1, 7] = bad
+    out, lse = r.run(q=spoilt.cuda())
+    assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+    keep = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    r.nb.sync()
+    assert torch.isfinite(out[keep]).all()
+    # the other rows' running maxima may be taken at other units: equal up to what rounding allows
+    out[0, 1], lse[0, 1] = clean[0, 1], clean_lse[0, 1]
+    r.check(out, lse)
+
+
+def test_two_handles_at_once_on_two_streams():
+    """A handle each: their launches share no tickets and no records."""
+    r = [Requests(51 + i, 8, 2, 128, 64, BF, [3000, 900], qs) for i, qs in enumerate([[1, 1], [40, 3]])]
+    alone = [x.run() for x in r]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in r]
+    for _ in range(10):
+        outs = []
+        for x, s in zip(r, streams):
+            with torch.cuda.stream(s):
+                outs.append(x.run())
+        torch.cuda.synchronize()
+        for a, b in zip(alone, outs):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("qs", [[1, 1, 1], [3, 1, 2], [40, 1, 90]])
 @pytest.mark.parametrize("temperature,scale", [(30.0, 0.0), (1.0, 0.7), (1e-3, 0.0), (3e4, 1e-4), (1e-5, 40.0)])
 def test_attention_over_query_sizes_and_scales(qs, temperature, scale):

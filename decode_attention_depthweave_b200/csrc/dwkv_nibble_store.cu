@@ -17,7 +17,7 @@ namespace dwkv {
 // cluster's threads, each finding its request by bisection of a prefix sum, so one long prompt
 // costs no more than many short ones.  The only dependency is pops and in-place updates after
 // pushes and reads: one cluster barrier.  Bound by latency, a dozen loads and barriers in a row: 9 us
-// for 8 requests of a row each, of which 6 are a launch's; 15 us for 1024 requests.
+// for 8 requests of a row each, 15 us for 1024 requests.
 // ------------------------------------------------------------------------------------
 constexpr int kTabThreads = 1024;                 // at most
 constexpr int kTabRows = 4;                       // rows in flight a thread

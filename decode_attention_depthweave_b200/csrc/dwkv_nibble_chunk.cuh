@@ -3,8 +3,8 @@
 //
 // A (256 rows x 128 tokens) unit at d = 128 is 2048 cycles of tcgen05.mma and as many of exponentials; it
 // takes 4900, bounded by the latencies and the issue slots of the softmax and unpacking warps (half of the
-// issue slots are used).  A chunk of 2048 rows of 32 heads, 8 kv-heads, at 32768 tokens: 1.13 to 1.16 ms,
-// 920 to 945 TFLOP/s (58 % of a large library matrix product's rate).  A CTA's warps:
+// issue slots are used).  A chunk of 2048 rows of 32 heads, 8 kv-heads, at 32768 tokens: 1.13 to 1.17 ms,
+// 910 to 945 TFLOP/s (56 to 58 % of a large library matrix product's rate).  A CTA's warps:
 //   0   MMA: S = Q K^T (from shared memory), O += P V (P from tensor memory).  The warp walks and waits
 //       together, one lane issues
 //   1   loader: bulk copies of the keys' and the values' half of each 16-token block

@@ -23,7 +23,8 @@ constexpr int kTabThreads = 1024;                 // at most
 constexpr int kTabRows = 4;                       // rows in flight a thread
 constexpr int kRowCap = 1 << 30;                 // the prefix sums saturate here
 
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kRowCap); }
+// Both operands are in [0, 2^30]: their sum needs 32 bits unsigned.
+__device__ __forceinline__ int sat_add(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kRowCap); }
 
 // Largest i in [0, n) with pre[i] <= x (pre ascending, pre[0] <= x).
 __device__ __forceinline__ int find_in(const int* pre, int n, int x) {

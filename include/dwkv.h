@@ -522,7 +522,7 @@ dwkv_status dwkv_nibble_destroy(dwkv_nibble_handle h);
  *     from the top of the stack, in slot order, and written behind the slot's pages in
  *     block_tables [n_seqs][max_blocks].
  * Outputs: seq_lens_out [n_seqs]; free_count_out [1]; cu_rows [n_seqs + 1], the running total of
- * n_new; positions (may be NULL) and slots [max_rows]: row cu_rows[b] + i has position len + i
+ * n_new, which stops at 2^30; positions (may be NULL) and slots [max_rows]: row cu_rows[b] + i has position len + i
  * and the slot that the tables give it; rows behind the last get -1 in both.  seq_lens_out may be
  * seq_lens and free_count_out may be free_count; apart from them no array overlaps another.
  * free_list has num_pages entries.

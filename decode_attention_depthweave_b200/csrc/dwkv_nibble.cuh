@@ -119,6 +119,11 @@ __device__ __forceinline__ void nib_error(const NibGeom& G, uint32_t code, uint3
     }
 }
 
+// The first token that a row at position p (below 0 where a request has more rows than tokens) sees.
+__device__ __forceinline__ int nib_first_seen(const NibGeom& G, int p) {
+    return G.window > 0 ? (int)max(0ll, (long long)p - G.window + 1) : 0;
+}
+
 // Length and query rows of slot b; false (and the device error word) where they cannot be.
 __device__ __forceinline__ bool nib_request(const NibGeom& G, const NibAttend& A, int b, int& len, int& nq) {
     const int c0 = A.cu[b], c1 = A.cu[b + 1];

@@ -76,7 +76,9 @@ NibGeom make_geom(const dwkv_nibble_config* c) {
     G.num_pages = c->num_pages;
     G.max_seqs = c->max_seqs;
     G.max_blocks = c->max_blocks;
-    G.window = c->window;
+    // A window that holds the longest request hides nothing.  What is left is below 2^30, as lengths are: positions minus
+    // a window stay in 32 bits.
+    G.window = c->window < (long long)c->max_blocks * c->page_tokens ? c->window : 0;
     G.fp16 = c->dtype == DWKV_FP16;
     G.tau = c->softmax_scale > 0.f ? c->softmax_scale : 1.0f / std::sqrt((float)c->head_dim);
     G.blk = nib_block_bytes(c->head_dim);

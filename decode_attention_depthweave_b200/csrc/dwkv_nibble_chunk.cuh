@@ -69,7 +69,7 @@ struct NcSpan {
 __device__ __forceinline__ void nc_item(const NibGeom& G, int len, int nq, int x, int& base, int& units) {
     const int rows = nq * G.g, r0 = 2 * kNcRows * x, r1 = min(rows, r0 + 2 * kNcRows);
     const int hi = len - nq + (r1 - 1) / G.g;
-    base = G.window > 0 ? max(0, len - nq + r0 / G.g - G.window + 1) & ~15 : 0;
+    base = nib_first_seen(G, len - nq + r0 / G.g) & ~15;
     units = max(1, (hi + 1 - base + kNcTokens - 1) / kNcTokens) + kNcBorder;
 }
 __device__ __forceinline__ NcSpan nc_span(const NibGeom& G, const NibAttend& A, int b) {

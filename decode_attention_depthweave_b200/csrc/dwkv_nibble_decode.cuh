@@ -142,7 +142,7 @@ __device__ __forceinline__ NdSpan nd_span(const NibGeom& G, const NibAttend& A, 
     NdSpan s{0, 0, 0, 0};
     if (b >= A.n) return s;
     if (!nib_request(G, A, b, s.len, s.nq) || s.nq == 0 || s.nq * G.g > A.rows_hi) { s.nq = 0; return s; }
-    s.base = G.window > 0 ? max(0, s.len - s.nq - G.window + 1) & ~15 : 0;
+    s.base = nib_first_seen(G, s.len - s.nq) & ~15;
     s.units = max(1, (s.len - s.base + kNdUnit - 1) / kNdUnit) + kNdBorder;
     return s;
 }

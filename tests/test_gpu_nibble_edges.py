@@ -34,3 +34,16 @@ def test_totals_of_refused_counts_stay_at_their_cap(new):
     base.step(nb, st, new, [b % 3 == 0 for b in range(n)], page, 64, in_place=False)
     with pytest.raises(dw.DwkvError, match="length or count|do not fit"):
         nb.sync()
+
+
+# ------------------------------------------------------------------------------ windows
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 16, 2**30, 4096, 1088, 1087, 1086])
+@pytest.mark.parametrize("lens,qs", [([2, 1000], [6, 1]), ([2, 0, 700], [3, 2, 1]), ([3, 1000], [200, 60]), ([0, 1, 1087], [40, 90, 1])])
+def test_windows_as_long_as_a_request_or_longer(window, lens, qs):
+    """Up to the largest that a configuration takes, with rows that stand before the first token."""
+    width = 17 - -(-max(lens) // 64)                              # rows of 17 pages: 1088 tokens
+    r = base.Requests(61, 8, 2, 128, 64, BF, lens, qs, window, extra_blocks=width)
+    assert r.nb.max_blocks == 17
+    out, lse = r.run()
+    r.nb.sync()
+    r.check(out, lse)

@@ -15,6 +15,7 @@ tensors too: a pool per layer, the tables and the lengths of a fixed set of requ
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import torch
@@ -130,6 +131,15 @@ def _raw(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _under(stream, device):
+    """A context in which torch allocates and works on `stream` (as in _raw; None: nothing changes)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 # cudaStream_t of a device's current stream, without building a Stream object where torch allows it
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -137,7 +147,9 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 class Nibble:
     """One handle on tensors that the caller owns.  Allocates the handle's arena, nothing else
-    (and outputs that are not passed in)."""
+    (and outputs that are not passed in).  A call's `stream` (a torch stream or a cudaStream_t; None:
+    the device's current one) is the one that the call works on: what it is given has to be ready there,
+    and the arena and outputs that are allocated here are tensors of that stream."""
 
     def __init__(self, cfg: dwkv_nibble_config, device="cuda", stream=None):
         if not torch.cuda.is_available():
@@ -150,7 +162,7 @@ class Nibble:
         self.pool_bytes = dwkv_nibble_pool_bytes(cfg)
         self.index, self.max_blocks, self.head_dim = self.device.index, cfg.max_blocks, cfg.head_dim
         self.num_q_heads, self.num_kv_heads = cfg.num_q_heads, cfg.num_kv_heads
-        with torch.cuda.device(self.device):
+        with torch.cuda.device(self.device), _under(stream, self.device):
             self.arena = torch.empty(dwkv_nibble_arena_bytes(cfg), dtype=torch.uint8, device=self.device)
             self.h = dwkv_nibble_create(cfg, self.arena, stream)
 
@@ -239,8 +251,9 @@ class Nibble:
         n = slots.numel()
         self._ints("slots", slots, n)
         self._pool(pool)
-        k = torch.empty(n, self.num_kv_heads, self.head_dim, dtype=self.dtype, device=self.device)
-        v = torch.empty_like(k)
+        with _under(stream, self.device):
+            k = torch.empty(n, self.num_kv_heads, self.head_dim, dtype=self.dtype, device=self.device)
+            v = torch.empty_like(k)
         dwkv_nibble_read(self.h, n, slots, pool, k, v, self._stream(stream))
         return k, v
 
@@ -254,7 +267,8 @@ class Nibble:
         self._table(block_tables, n)
         self._pool(pool)
         if out is None:
-            out = torch.empty(rows, hq, d, dtype=self.dtype, device=self.device)
+            with _under(stream, self.device):
+                out = torch.empty(rows, hq, d, dtype=self.dtype, device=self.device)
         elif self._rows("out", out, hq) != (rows, hq * d):
             raise ValueError("out must be contiguous and have q's rows")
         if lse is not None:
@@ -262,7 +276,8 @@ class Nibble:
                     lse.numel() != rows * hq:
                 raise ValueError(f"lse must be contiguous float32 [{rows}][{hq}] on {self.device}")
         elif want_lse:
-            lse = torch.empty(rows, hq, dtype=torch.float32, device=self.device)
+            with _under(stream, self.device):
+                lse = torch.empty(rows, hq, dtype=torch.float32, device=self.device)
         dwkv_nibble_attention(self.h, n, rows, int(max_q), q, qs, cu_rows, seq_lens, block_tables, pool, out, lse,
                               self._stream(stream))
         return out if lse is None else (out, lse)
@@ -275,7 +290,7 @@ class Nibble:
 class NibbleCache:
     """A 4-bit cache of `num_layers` layers for `max_seqs` request slots: the pools, the tables
     and a handle.  step() places the rows of a step; append() and attention() then take them
-    layer by layer."""
+    layer by layer.  The tensors are made, and cleared, on the constructor's `stream`."""
 
     def __init__(self, num_layers, num_q_heads, num_kv_heads, head_dim, num_pages, max_seqs, max_context, page_tokens=64,
                  max_rows=None, dtype=torch.bfloat16, window=0, softmax_scale=0.0, device="cuda", stream=None):
@@ -284,16 +299,17 @@ class NibbleCache:
                                              dtype, window, softmax_scale), device, stream)
         dev = self.device = self.ops.device
         self.num_layers, self.max_seqs = num_layers, max_seqs
-        self.pools = torch.zeros(num_layers, self.ops.pool_bytes, dtype=torch.uint8, device=dev)
 
         def ints(*shape):
             return torch.zeros(*shape, dtype=torch.int32, device=dev)
-        self.seq_lens, self.block_tables = ints(max_seqs), ints(max_seqs, blocks)
-        self.free_list = torch.arange(num_pages, dtype=torch.int32, device=dev)
-        self.free_count = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
-        self.cu_rows = ints(max_seqs + 1)
         rows = max_rows or max_seqs
-        self.positions, self.slots = ints(rows), ints(rows)
+        with _under(stream, dev):
+            self.pools = torch.zeros(num_layers, self.ops.pool_bytes, dtype=torch.uint8, device=dev)
+            self.seq_lens, self.block_tables = ints(max_seqs), ints(max_seqs, blocks)
+            self.free_list = torch.arange(num_pages, dtype=torch.int32, device=dev)
+            self.free_count = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
+            self.cu_rows = ints(max_seqs + 1)
+            self.positions, self.slots = ints(rows), ints(rows)
 
     def close(self):
         self.ops.close()
@@ -319,9 +335,10 @@ class NibbleCache:
     def read(self, layer, seq, length, stream=None):
         """(k, v) [length][Hkv][d]: the first `length` tokens of a slot, as stored."""
         p = self.ops.cfg.page_tokens
-        t = torch.arange(length, device=self.device)
-        slots = self.block_tables[seq, t // p] * p + (t % p).to(torch.int32)
-        return self.ops.read(slots.to(torch.int32), self.pools[layer], stream)
+        with _under(stream, self.device):                 # after the steps on that stream, and kept for it
+            t = torch.arange(length, device=self.device)
+            slots = (self.block_tables[seq, t // p] * p + (t % p).to(torch.int32)).to(torch.int32)
+            return self.ops.read(slots, self.pools[layer], stream)
 
     def sync(self, stream=None):
         self.ops.sync(stream)

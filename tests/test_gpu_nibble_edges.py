@@ -47,3 +47,69 @@ def test_windows_as_long_as_a_request_or_longer(window, lens, qs):
     out, lse = r.run()
     r.nb.sync()
     r.check(out, lse)
+
+
+# ------------------------------------------------------------------------------ streams
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_stream_of_its_own_while_another_is_current(raw):
+    """step, append, attention and read on a stream that is given and not current, with work pending on
+    both: nothing of a call is done on the current stream, and no memory that the current one still uses is
+    taken for it."""
+    hq, hkv, d, rows = 8, 2, 128, 500
+    g = torch.Generator().manual_seed(71)
+    qkv = torch.randn(rows, hq + 2 * hkv, d, generator=g).to(BF).cuda()
+    new = i32([300, 200])
+
+    def run(c, stream):
+        c.step(new, stream=stream)
+        c.append(0, qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], stream=stream)
+        out, lse = c.attention(0, qkv[:, :hq], 300, want_lse=True, stream=stream)
+        return (out, lse, *c.read(0, 0, 300, stream=stream), *c.read(0, 1, 200, stream=stream))
+
+    def cache(stream):
+        return dw.NibbleCache(1, hq, hkv, d, num_pages=40, max_seqs=2, max_context=512, page_tokens=32, max_rows=rows, stream=stream)
+    want = run(cache(None), None)                                 # also loads what torch loads at first use
+    torch.cuda.synchronize()
+    for late in ("given", "current"):
+        s = torch.cuda.Stream()
+        stream = s.cuda_stream if raw else s
+        # of the current stream: blocks of the outputs' sizes, freed with their last use pending
+        filled = [torch.empty_like(x) for x in want]
+        with torch.cuda.stream(s) if late == "given" else torch.cuda.stream(torch.cuda.current_stream()):
+            torch.cuda._sleep(40_000_000)
+        for x in filled:
+            x.fill_(7)
+        del x, filled
+        c = cache(stream)
+        if late == "given":
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(40_000_000)                     # the step is late: what reads its tables waits for it
+        got = run(c, stream)
+        s.synchronize()
+        copies = [x.cpu() for x in got]                           # (waits for the current stream's work too)
+        torch.cuda.synchronize()
+        for a, b, e in zip(want, got, copies):
+            assert torch.equal(a, b) and torch.equal(a.cpu(), e)
+        c.sync(stream)
+
+
+def test_a_stream_for_the_wrappers_outputs():
+    """Outputs that attention and read allocate are memory of the given stream: not a block that pending work
+    of the current one still writes."""
+    r = base.Requests(72, 8, 2, 128, 64, BF, [900, 333], [1, 1])
+    want, want_lse = r.run()
+    dev = [i32(x) for x in (r.cu, r.lens, r.table.tolist())]
+    q, slots = r.q.cuda(), torch.arange(128, dtype=torch.int32, device="cuda")
+    k, v = r.nb.read(slots, r.dev_pool)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.empty_like(x) for x in (want, want_lse, k, v)]
+        torch.cuda._sleep(40_000_000)
+        for x in old:
+            x.zero_()
+        del x, old
+        out, lse = r.nb.attention(q, *dev, r.dev_pool, 1, want_lse=True, stream=s)
+        rk, rv = r.nb.read(slots, r.dev_pool, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(rk, k) and torch.equal(rv, v)

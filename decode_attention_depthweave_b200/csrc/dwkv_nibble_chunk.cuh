@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 named_barrier(1 + t, kNcTile);
                 a = fmaxf(a, place[(hc ^ 1) * kNcRows + r]);
                 const uint32_t e = min(max(__float_as_uint(a) >> 23, 1u), 253u);
-                const float sc = __uint_as_float((254u - e) << 23);
+                // an infinite query has no softmax, even where all its scores are -inf: NaN from here on
+                const float sc = a < INFINITY ? __uint_as_float((254u - e) << 23) : __uint_as_float(0x7fc00000u);
                 // not 0, however small the scale: a masked score is -inf times it
                 fac = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
                 uint8_t* dst = sm + L::kQ + t * L::kTile + r * 128;

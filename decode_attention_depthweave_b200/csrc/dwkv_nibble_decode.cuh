@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 1));
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
             const uint32_t e = min(max(__float_as_uint(a) >> 23, 1u), 253u);
-            const float sc = __uint_as_float((254u - e) << 23);
+            // an infinite query has no softmax, even where all its scores are -inf: NaN from here on
+            const float sc = a < INFINITY ? __uint_as_float((254u - e) << 23) : __uint_as_float(0x7fc00000u);
 #pragma unroll
             for (int x = 0; x < kWords; ++x) {
                 float f[8];

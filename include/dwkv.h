@@ -566,7 +566,9 @@ dwkv_status dwkv_nibble_read(dwkv_nibble_handle h, int32_t n_rows, const int32_t
  *         (DWKV_DEV_BAD_LENGTH).  Tokens in a page outside the pool are left out
  *         (DWKV_DEV_BAD_PAGE).  Should the lengths times num_kv_heads add up to 2^38 tokens or
  *         more, nothing may be computed (DWKV_DEV_BAD_LENGTH).
- * A query that is NaN or infinite makes its own row and head NaN.  What lies in the pool behind a request's last token is not looked at, NaN patterns included. */
+ * A query that is NaN or infinite makes its own row and head NaN (out and lse) if the row sees a
+ * token.  What lies in the pool behind a request's last token is not looked at, NaN patterns
+ * included. */
 dwkv_status dwkv_nibble_attention(dwkv_nibble_handle h, int32_t n_seqs, int32_t n_rows, int32_t max_q, const void* q,
                                   int64_t q_stride, const int32_t* cu_rows, const int32_t* seq_lens,
                                   const int32_t* block_tables, const void* pool, void* out, float* lse, void* stream);

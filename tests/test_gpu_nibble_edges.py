@@ -113,3 +113,39 @@ def test_a_stream_for_the_wrappers_outputs():
         rk, rv = r.nb.read(slots, r.dev_pool, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(rk, k) and torch.equal(rv, v)
+
+
+# ------------------------------------------------------------------------------ queries
+def one_request(hq, d, dtype, k, v, q, scale=0.0, page=16):
+    """Attention of the rows q [rows][hq][d] over the tokens k, v [tokens][d] of one kv-head: (out, lse) and
+    what ref.attention gives for the stored values."""
+    n, rows = k.shape[0], q.shape[0]
+    blocks = -(-n // page)
+    nb = ops(hq, 1, d, page, blocks, 1, blocks, dtype, 0, scale)
+    pool = torch.zeros(nb.pool_bytes, dtype=torch.uint8, device="cuda")
+    nb.append(k[:, None].to(dtype).cuda(), v[:, None].to(dtype).cuda(), torch.arange(n, dtype=torch.int32, device="cuda"), pool)
+    q = q.to(dtype)
+    out, lse = nb.attention(q.cuda(), i32([0, rows]), i32([n]), i32([list(range(blocks))]), pool, rows, want_lse=True)
+    nb.sync()
+    want = ref.attention(q, [0, rows], [n], [list(range(blocks))], pool.cpu().numpy(), 1, page, 0, scale)
+    return out.double().cpu().numpy(), lse.double().cpu().numpy(), want
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("hq,rows", [(4, 1), (4, 2), (4, 4), (4, 7), (4, 10), (40, 2)])
+@pytest.mark.parametrize("tokens", [1, 2, 3])
+def test_an_infinite_query_over_few_tokens(d, bad, hq, rows, tokens):
+    """Whatever the sign of the scores, the row is NaN if it sees a token, and 0 (lse -inf) if it sees none."""
+    g = torch.Generator().manual_seed(tokens)
+    for sign in (1.0, -1.0):
+        k = torch.randn(tokens, d, generator=g)
+        k[:, 7] = 3 * sign
+        q = torch.randn(rows, hq, d, generator=g)
+        q[:, 1, 7] = bad
+        out, lse, _ = one_request(hq, d, BF, k, torch.ones(tokens, d), q)
+        sees = tokens - rows + np.arange(rows) >= 0
+        assert np.isnan(out[sees, 1]).all() and np.isnan(lse[sees, 1]).all()
+        assert (out[~sees, 1] == 0).all() and np.isneginf(lse[~sees, 1]).all()
+        rest = np.arange(hq) != 1
+        assert np.isfinite(out[:, rest]).all() and np.isfinite(lse[sees][:, rest]).all()

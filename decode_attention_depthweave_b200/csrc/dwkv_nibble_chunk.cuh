@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
             const int row0 = A.cu[w.b];
             const bool have = row < rows;
             const int jq = have ? row / G.g : 0, hg = have ? row - jq * G.g : 0;
-            // ---- the query row, scaled by a power of two to below 2, as fp16; half a row a thread
+            // ---- the query row, as nib_query_scale says; half a row a thread
             float fac;
             {
                 const uint16_t* qp = A.q + (size_t)(row0 + jq) * A.q_stride + (size_t)(w.h * G.g + hg) * D + hc * (D / 2);
@@ -568,11 +568,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 place[hc * kNcRows + r] = a;
                 named_barrier(1 + t, kNcTile);
                 a = fmaxf(a, place[(hc ^ 1) * kNcRows + r]);
-                const uint32_t e = min(max(__float_as_uint(a) >> 23, 1u), 253u);
-                // an infinite query has no softmax, even where all its scores are -inf: NaN from here on
-                const float sc = a < INFINITY ? __uint_as_float((254u - e) << 23) : __uint_as_float(0x7fc00000u);
-                // not 0, however small the scale: a masked score is -inf times it
-                fac = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
+                const float sc = nib_query_scale(G, a, fac);
                 uint8_t* dst = sm + L::kQ + t * L::kTile + r * 128;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {

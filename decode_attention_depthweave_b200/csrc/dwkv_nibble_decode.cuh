@@ -130,6 +130,17 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
 
+// Queries enter the products as fp16, each row times the power of two that brings its largest magnitude a
+// to [2^15, 2^16).  That is exact for fp16 rows (they only grow) and for bf16 ones down to 2^-32 of a; what is
+// smaller errs by at most 2^-40 a.  Returns the factor; fac: from a score of such rows and of values in units of 32
+// to log2 units, never 0, since a masked score is -inf times it.
+__device__ __forceinline__ float nib_query_scale(const NibGeom& G, float a, float& fac) {
+    const uint32_t e = min(max(__float_as_uint(a) >> 23, 15u), 254u);
+    fac = fmaxf(G.tau * 1.4426950408889634f * 0x1p-10f * __uint_as_float(e << 23), 1.17549435e-38f);
+    // an infinite query has no softmax, even where all its scores are -inf: NaN from here on
+    return a < INFINITY ? __uint_as_float((269u - e) << 23) : __uint_as_float(0x7fc00000u);
+}
+
 // Empty units counted behind each (request, kv-head): what its end costs a CTA (merging the warps,
 // writing, the next one's queries) in units, so that ranges with an end in them carry less.
 constexpr int kNdBorder = 1;
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
     for (bool more = true; more; more = w.next(G, A, lane)) {
         const int cnt = w.count(), rows = w.nq * G.g;
         const int row0 = A.cu[w.b];
-        // queries as B fragments, each row scaled by a power of two to below 2 (exact in fp16)
+        // queries as B fragments, each row as nib_query_scale says
         uint4* qs = reinterpret_cast<uint4*>(sm + L::kQ) + lane;
         float fac[NT][2];                                // unscaled score -> log2 units, for the lane's columns
         int pos[NT][2];                                  // position of the lane's columns' rows
@@ -389,9 +400,8 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
             }
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 1));
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
-            const uint32_t e = min(max(__float_as_uint(a) >> 23, 1u), 253u);
-            // an infinite query has no softmax, even where all its scores are -inf: NaN from here on
-            const float sc = a < INFINITY ? __uint_as_float((254u - e) << 23) : __uint_as_float(0x7fc00000u);
+            float mult;
+            const float sc = nib_query_scale(G, a, mult);
 #pragma unroll
             for (int x = 0; x < kWords; ++x) {
                 float f[8];
@@ -404,8 +414,6 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                     qs[(nt * kWords + x) * 32] = make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]),
                                                             pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
             }
-            // not 0, however small the scale: a masked score is -inf times it
-            const float mult = fmaxf(G.tau * 1.4426950408889634f * 32.f * __uint_as_float(e << 23), 1.17549435e-38f);
             fac[nt][0] = __shfl_sync(~0u, mult, 8 * i);
             fac[nt][1] = __shfl_sync(~0u, mult, 8 * i + 4);
 #pragma unroll

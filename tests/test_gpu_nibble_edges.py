@@ -149,3 +149,49 @@ def test_an_infinite_query_over_few_tokens(d, bad, hq, rows, tokens):
         assert (out[~sees, 1] == 0).all() and np.isneginf(lse[~sees, 1]).all()
         rest = np.arange(hq) != 1
         assert np.isfinite(out[:, rest]).all() and np.isfinite(lse[sees][:, rest]).all()
+
+
+def exact_query_tolerances(o, lse, mag, span, d, dtype):
+    """ref.tolerances without its term for query channels that lose their tail."""
+    es = span * (d * 2.0 ** -23 + 2.0 ** -21) + 2.0 ** -21
+    half = torch.finfo(dtype).eps / 2
+    to = mag * (2.0 ** -11 + 2.0 ** -20 + 2 * es[..., None]) + half * np.abs(o) * (1 + 2.0 ** -8) + 2.0 ** -25
+    return to, es + 2.0 ** -20 + np.abs(lse) * 2.0 ** -22
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,small", [(BF, 10), (BF, 17), (BF, 20), (BF, 24), (BF, 31), (FP, 10), (FP, 14), (FP, 16), (FP, 22)])
+@pytest.mark.parametrize("hq,rows", [(4, 1), (4, 2), (4, 4), (4, 8), (4, 40)])
+def test_small_channels_of_a_query_count(d, dtype, small, hq, rows):
+    """16 channels of the queries far below the others, with keys as far above theirs: their products are the
+    larger ones, and no bit of the 16-bit queries is lost.  (fp16 queries reach down to 2^-24; bf16 magnitudes
+    from 1 to 2 times 2^-small, all within 2^-32 of the row's largest, 1.)"""
+    g = torch.Generator().manual_seed(small)
+    n = 70
+    k, v = torch.randn(n, d, generator=g) * 2.0 ** -10, torch.randn(n, d, generator=g)
+    k[:, 16:32] = torch.randn(n, 16, generator=g).clamp(-4, 4) * 2.0 ** 13
+    sign = torch.randint(0, 2, (rows, hq, d), generator=g) * 2.0 - 1
+    q = torch.rand(rows, hq, d, generator=g) * sign
+    q[:, :, 0] = 1
+    q[:, :, 16:32] = (1 + torch.rand(rows, hq, 16, generator=g)) * sign[:, :, 16:32] * 2.0 ** -small
+    out, lse, (o, l, mag, span) = one_request(hq, d, dtype, k, v, q)
+    sees = np.isfinite(l)
+    to, tl = exact_query_tolerances(o, np.where(sees, l, 0), mag, span, d, dtype)
+    assert (np.abs(lse - l)[sees] <= tl[sees]).all(), (np.abs(lse - l)[sees] / tl[sees]).max()
+    assert (np.abs(out - o) <= to).all(), (np.abs(out - o) / to).max()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 4, 8, 40])
+@pytest.mark.parametrize("largest", [2.0 ** 127, 2.0 ** 60, 2.0 ** -100, 2.0 ** -126, 2.0 ** -133])
+def test_queries_of_any_magnitude(rows, largest):
+    """Rows whose largest channel is at either end of bf16: scores from the smallest keys."""
+    g = torch.Generator().manual_seed(rows)
+    n, d, hq = 40, 128, 4
+    k, v = torch.randn(n, d, generator=g) * 2.0 ** -14, torch.randn(n, d, generator=g)
+    q = (torch.rand(rows, hq, d, generator=g) * 2 - 1) * largest
+    q[:, :, 0] = largest
+    scale = min(2.0 ** 10 / largest, 2.0 ** 100)
+    out, lse, (o, l, mag, span) = one_request(hq, d, BF, k, v, q, scale)
+    sees = np.isfinite(l)
+    to, tl = exact_query_tolerances(o, np.where(sees, l, 0), mag, span, d, BF)
+    assert (np.abs(lse - l)[sees] <= tl[sees]).all() and (np.abs(out - o) <= to).all()

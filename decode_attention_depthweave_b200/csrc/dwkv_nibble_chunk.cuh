@@ -628,27 +628,40 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 uint32_t pk[32];
                 float sum, top;
                 for (bool again = false;;) {             // a second time when the maximum moves
-                    const float2 c0 = make_float2(kNdBias - m, kNdBias - m), f2 = make_float2(fac, fac);
-                    float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    top = -INFINITY;
+                    // the scores' weights, their sum and the largest score; far: some row's maximum is (nib_far)
+                    auto weigh = [&](auto far_) {
+                        constexpr bool kFar = decltype(far_)::value;
+                        const bool far = kFar && nib_far(m);
+                        const float cc = far ? kNdBias : kNdBias - m, ff = far ? 1.f : fac;
+                        const float2 c0 = make_float2(cc, cc), f2 = make_float2(ff, ff);
+                        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float x[32];
-                        nc_ld32(s_at + 32 * c, x);
-                        mask(x, c);
-                        float tops[2] = {-INFINITY, -INFINITY};
+                        for (int c = 0; c < 2; ++c) {
+                            float x[32];
+                            nc_ld32(s_at + 32 * c, x);
+                            mask(x, c);
+                            float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) {
-                            tops[(y >> 1) & 1] = fmaxf(tops[(y >> 1) & 1], fmaxf(x[y], x[y + 1]));
-                            const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
-                            const float2 p = make_float2(ex2(z.x), ex2(z.y));
-                            sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
-                            pk[16 * c + y / 2] = pack_half2(p.x, p.y);
+                            for (int y = 0; y < 32; y += 2) {
+                                tops[(y >> 1) & 1] = fmaxf(tops[(y >> 1) & 1], fmaxf(x[y], x[y + 1]));
+                                if (far) {
+                                    x[y] = nib_far_weight(x[y], fac, m);
+                                    x[y + 1] = nib_far_weight(x[y + 1], fac, m);
+                                }
+                                const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
+                                const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                                sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
+                                pk[16 * c + y / 2] = pack_half2(p.x, p.y);
+                            }
+                            top = fmaxf(top, fmaxf(tops[0], tops[1]));
                         }
-                        top = fmaxf(top, fmaxf(tops[0], tops[1]));
-                    }
-                    const float2 sa = add2(sums[0], sums[1]);
-                    sum = sa.x + sa.y;
+                        const float2 sa = add2(sums[0], sums[1]);
+                        sum = sa.x + sa.y;
+                    };
+                    const bool any_far = __any_sync(~0u, nib_far(m));
+                    if (any_far) weigh(std::true_type{});
+                    else weigh(std::false_type{});
                     if (again) break;
                     // the row's maximum over both halves; two places in turn, so that one barrier a unit will do
                     float* place = ex + (units & 1u) * 4 * kNcRows;
@@ -656,7 +669,7 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     named_barrier(1 + t, kNcTile);
                     top = fmaxf(top, place[(hc ^ 1) * kNcRows + r]);
                     const float mx = top > -INFINITY ? top * fac : kNdNone;
-                    if (!__any_sync(~0u, mx > m + kNdLag)) break;
+                    if (!__any_sync(~0u, mx > (any_far ? m : m + kNdLag))) break;
                     again = true;
                     const float mn = fmaxf(m, mx), f = ex2(m - mn);
                     m = mn;

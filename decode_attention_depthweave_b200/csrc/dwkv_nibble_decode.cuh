@@ -25,6 +25,9 @@
 //    and in the value product what the rounding left, so P is good to 22 bits.
 //  - P carries 2^7: with the maximum allowed to lag 2^8 behind, it stays below 2^15, and weights
 //    down to 2^-31 keep a bit.
+//  - Weights are 2^(s fac - m) by one fma with the rounded m = s_max fac.  From |m| = 2^21 on that rounding, the
+//    same for all of a row, could carry P out of fp16: such rows take s fac rounded as m is, with no lag, so that
+//    the largest weight is 1 again.  (Scores of a million and more: a branch that others do not enter.)
 #pragma once
 #include "dwkv_nibble.cuh"
 
@@ -38,8 +41,9 @@ constexpr int kNdThreads = 32 * kNdWarps;               // consumers; one more w
 constexpr int kNdSub = 2;                                // blocks that a warp takes at a time
 constexpr int kNdBlocks = kNdSub * kNdWarps;             // blocks of a unit
 constexpr int kNdUnit = kNibBlock * kNdBlocks;           // tokens of a unit
-constexpr float kNdNone = -1e30f;                        // maximum of nothing
+constexpr float kNdNone = -3.402823466e38f;              // maximum of nothing
 constexpr float kNdLag = 8.f, kNdBias = 7.f;             // log2
+constexpr float kNdFar = 2097152.f;                      // log2
 
 template <int D, int R>
 struct NdLayout {
@@ -140,6 +144,10 @@ __device__ __forceinline__ float nib_query_scale(const NibGeom& G, float a, floa
     // an infinite query has no softmax, even where all its scores are -inf: NaN from here on
     return a < INFINITY ? __uint_as_float((269u - e) << 23) : __uint_as_float(0x7fc00000u);
 }
+
+// A row's maximum is so large that its scores are rounded before it is taken from them.
+__device__ __forceinline__ bool nib_far(float m) { return fabsf(m) >= kNdFar && m > kNdNone; }
+__device__ __forceinline__ float nib_far_weight(float s, float fac, float m) { return __fadd_rn(__fmul_rn(s, fac), -m); }
 
 // Empty units counted behind each (request, kv-head): what its end costs a CTA (merging the warps,
 // writing, the next one's queries) in units, so that ranges with an end in them carry less.
@@ -431,6 +439,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
 #pragma unroll
             for (int x = 0; x < 2 * kChunks; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
         }
+        bool far = false;                                // of any of the warp's rows
         named_barrier(1, kNdThreads);
         int t0 = w.base + w.unit * kNdUnit + kNdSub * 16 * warp;
         for (int u = 0; u < cnt; ++u, t0 += kNdUnit) {
@@ -516,6 +525,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
 #pragma unroll
                         for (int x = 0; x < 4; ++x) jump |= s[k][nt][x] > thr[nt][x & 1];
                 if (__any_sync(~0u, jump)) {             // the maximum moves: all rows take the new one
+                    far = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -528,7 +538,8 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                             x = fmaxf(m[nt][c], fac[nt][c] * fmaxf(x, __shfl_xor_sync(~0u, x, 16)));
                             const float f = ex2(m[nt][c] - x);
                             m[nt][c] = x;
-                            thr[nt][c] = x > kNdNone ? (x + kNdLag) / fac[nt][c] : -INFINITY;
+                            thr[nt][c] = x > kNdNone && !nib_far(x) ? (x + kNdLag) / fac[nt][c] : -INFINITY;
+                            far |= nib_far(x);
                             l[nt][c] *= f;
 #pragma unroll
                             for (int y = 0; y < 2 * kChunks; ++y) {
@@ -536,6 +547,27 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                                 o[nt][y][c + 2] *= f;
                             }
                         }
+                    far = __any_sync(~0u, far);
+                }
+                // the weights' logarithms
+                if (!far) {
+#pragma unroll
+                    for (int k = 0; k < kNdSub; ++k)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) s[k][nt][x] = fmaf(s[k][nt][x], fac[nt][x & 1], kNdBias - m[nt][x & 1]);
+                } else {
+                    asm volatile("" ::: "memory");
+#pragma unroll
+                    for (int k = 0; k < kNdSub; ++k)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float f = fac[nt][x & 1], mm = m[nt][x & 1];
+                                s[k][nt][x] = nib_far(mm) ? kNdBias + nib_far_weight(s[k][nt][x], f, mm) : fmaf(s[k][nt][x], f, kNdBias - mm);
+                            }
                 }
 #pragma unroll
                 for (int k = 0; k < kNdSub; ++k) {
@@ -545,7 +577,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                         float pr[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            pr[x] = ex2(fmaf(s[k][nt][x], fac[nt][x & 1], kNdBias - m[nt][x & 1]));
+                            pr[x] = ex2(s[k][nt][x]);
                             l[nt][x & 1] += pr[x];
                         }
 #pragma unroll

@@ -195,3 +195,35 @@ def test_queries_of_any_magnitude(rows, largest):
     sees = np.isfinite(l)
     to, tl = exact_query_tolerances(o, np.where(sees, l, 0), mag, span, d, BF)
     assert (np.abs(lse - l)[sees] <= tl[sees]).all() and (np.abs(out - o) <= to).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,size", [(BF, 1e2), (BF, 3e3), (BF, 1e5), (BF, 1e7), (BF, 1e30), (FP, 3e3), (FP, 1.5e4)])
+@pytest.mark.parametrize("hq,rows,n", [(4, 1, 70), (4, 2, 70), (16, 1, 70), (4, 8, 70), (4, 40, 70), (4, 1, 4000), (4, 8, 4000), (4, 70, 4000)])
+def test_scores_of_any_magnitude(d, dtype, size, hq, rows, n):
+    """Scores of 10^5 to 10^34, of either sign.  A score errs by at most span (d 2^-23 + 2^-21), so that only tokens
+    within twice that of the largest one (and 40 below it, whose weights are below 2^-57) have a weight: each output
+    lies between their smallest and largest value, give or take the rounding of weights (2^-11 of the largest value)
+    and of the output.  Odd heads see negative scores only."""
+    g = torch.Generator().manual_seed(n + rows)
+    k, v = torch.randn(n, d, generator=g), torch.randn(n, d, generator=g)
+    k = k * torch.linspace(0.2, 1, n)[:, None] * 6000             # the maximum moves along the tokens
+    k[:, 0] = 20000 + 100 * torch.randn(n, generator=g)
+    q = torch.randn(rows, hq, d, generator=g).clamp(-4, 4) * size
+    q[:, 1::2] *= 0.01
+    q[:, 1::2, 0] = -size
+    out, lse, (o, l, mag, span) = one_request(hq, d, dtype, k, v, q)
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    x, keys, vals = q.to(dtype).double().numpy(), *(ref.values(*ref.quantise(y.to(dtype).double().numpy())) for y in (k, v))
+    es = span * (d * 2.0 ** -23 + 2.0 ** -21) + 2.0 ** -21
+    off, half = [], torch.finfo(dtype).eps / 2
+    for r in range(rows):
+        upto = n - rows + r + 1
+        s = x[r] @ keys[:upto].T / d ** 0.5
+        for h in range(hq):
+            alive = vals[:upto][s[h] >= s[h].max() - 2 * es[r, h] - 40]
+            lo, hi = alive.min(0), alive.max(0)
+            slack = (2.0 ** -11 + 2.0 ** -15) * np.abs(alive).max() + half * np.abs(out[r, h]) * (1 + 2.0 ** -8)
+            off.append(max(((lo - slack) - out[r, h]).max(), (out[r, h] - (hi + slack)).max()))
+    assert max(off) <= 0
+    assert (np.abs(lse - l) <= es + 2.0 ** -20 + np.abs(l) * 2.0 ** -22).all()

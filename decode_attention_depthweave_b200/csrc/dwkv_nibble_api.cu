@@ -255,7 +255,7 @@ dwkv_status dwkv_nibble_attention(dwkv_nibble_handle h, int32_t n_seqs, int32_t 
     if (n_seqs < 0 || n_seqs > G.max_seqs)
         return fail(DWKV_ERR_INVALID_ARG, "n_seqs %d out of [0, %d]", n_seqs, G.max_seqs);
     if (n_rows < 0 || max_q < 0) return fail(DWKV_ERR_INVALID_ARG, "n_rows %d or max_q %d is negative", n_rows, max_q);
-    if (n_seqs == 0 || n_rows == 0 || max_q == 0) return DWKV_OK;
+    if (n_seqs == 0 || n_rows == 0) return DWKV_OK;      // with max_q 0, requests that have rows are still recorded
     if (!q || !cu_rows || !seq_lens || !block_tables || !out)
         return fail(DWKV_ERR_INVALID_ARG, "q, cu_rows, seq_lens, block_tables and out must be non-NULL");
     if (misaligned(q, 16) || misaligned(out, 16)) return fail(DWKV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");

@@ -227,3 +227,17 @@ def test_scores_of_any_magnitude(d, dtype, size, hq, rows, n):
             off.append(max(((lo - slack) - out[r, h]).max(), (out[r, h] - (hi + slack)).max()))
     assert max(off) <= 0
     assert (np.abs(lse - l) <= es + 2.0 ** -20 + np.abs(l) * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_rows_beside_a_max_q_of_zero_are_recorded(n):
+    r = base.Requests(81, 4, 1, 128, 64, BF, [20] * n, [1] + [0] * (n - 1))
+    out = torch.full((1, 4, 128), 7.0, dtype=BF, device="cuda")
+    r.run(out=out, max_q=0)
+    with pytest.raises(dw.DwkvError, match="do not fit"):
+        r.nb.sync()
+    assert out.eq(7).all()
+    r.cu = [0] * (n + 1)                                          # no request has rows: nothing to record
+    r.run(out=out, max_q=0)
+    r.nb.sync()
+    assert out.eq(7).all()

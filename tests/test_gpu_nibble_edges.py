@@ -241,3 +241,56 @@ def test_rows_beside_a_max_q_of_zero_are_recorded(n):
     r.run(out=out, max_q=0)
     r.nb.sync()
     assert out.eq(7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,rows", [(1, 1), (4, 1), (2, 2), (1, 4)])
+def test_fp16_outputs_of_up_to_4_rows_take_weights_of_22_bits(d, hq, rows):
+    """Weights whose rounding to 11 bits all errs the same way against values that all but cancel.  24 tokens are
+    one warp's first unit: a weight is 2^(s - max + 7), in two fp16 parts.  Each errs by at most 2^-22 of itself
+    (both parts above 2^-14 here); ref.tolerances with that in place of 2^-11 is a bound that 11 bits fail."""
+    g = torch.Generator().manual_seed(d + hq)
+    n, h, r = 24, hq - 1, rows - 1                                # the row that the values are made for sees all tokens
+    k = torch.randn(n, d, generator=g)
+    q = (torch.randn(rows, hq, d, generator=g) * 0.01).to(FP)
+    stored = ref.values(*ref.quantise(k.to(FP).double().numpy()))
+    s = q[r, h].double().numpy() @ stored.T / d ** 0.5 * np.log2(np.e)
+    p = np.exp2(s - s.max() + 7)
+    err = p.astype(np.float16).astype(np.float64) - p
+    v = np.where(err > 0, 1.0, -1.0)
+    for t in np.argsort(np.abs(err)):                             # turn the least wrong ones until the values cancel
+        if abs((p * v).sum() - 2 * p[t] * v[t]) < abs((p * v).sum()):
+            v[t] = -v[t]
+    v = torch.from_numpy(np.repeat(v[:, None], d, 1))
+    out, lse, (o, l, mag, span) = one_request(hq, d, FP, k, v, q)
+    to, _ = ref.tolerances(o, np.where(np.isfinite(l), l, 0), mag, span, d, FP)
+    to = to - mag * (2.0 ** -11 - 2.0 ** -22)
+    rounded = (p + err) @ ref.values(*ref.quantise(v.numpy())) / p.sum()
+    assert (np.abs(rounded - o[r, h]) > 2 * to[r, h]).all()       # what 11 bits would give is outside the bound
+    assert (np.abs(out - o) <= to).all(), (np.abs(out - o) / to).max()
+
+
+# ------------------------------------------------------------------------------ append and read
+@pytest.mark.parametrize("d,hkv,dtype", [(128, 8, FP), (128, 9, BF), (128, 17, FP), (64, 16, BF), (64, 17, FP), (64, 33, BF)])
+def test_append_and_read_of_more_heads_than_a_warp_takes_at_once(d, hkv, dtype):
+    rng = np.random.default_rng(hkv)
+    page, pages, n = 16, 3, 9
+    nb = ops(hkv, hkv, d, page, pages, dtype=dtype)
+    want = rng.integers(0, 256, nb.pool_bytes, dtype=np.uint8)
+    pool = torch.from_numpy(want.copy()).cuda()
+    slots = rng.permutation(pages * page)[:n].astype(np.int32)
+    slots[4] = -1
+    x = torch.from_numpy(rng.standard_normal((2, n, hkv, d)) * np.exp(rng.uniform(-4, 4, (2, n, hkv, 1)))).to(dtype)
+    nb.append(x[0].cuda(), x[1].cuda(), torch.from_numpy(slots).cuda(), pool)
+    got = nb.read(torch.from_numpy(slots).cuda(), pool)
+    nb.sync()
+    for z in range(2):
+        c, b = ref.quantise(x[z].double().numpy())
+        val = ref.values(c, b)
+        val[slots < 0] = 0
+        assert np.array_equal(got[z].double().cpu().numpy(), val)
+        for i, s in enumerate(slots):
+            for h in range(hkv):
+                if s >= 0:
+                    ref.put(want, hkv, page, d, int(s), h, z, c[i, h], b[i, h])
+    assert np.array_equal(pool.cpu().numpy(), want)

@@ -627,41 +627,29 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                 };
                 uint32_t pk[32];
                 float sum, top;
+                float zf = fac, zc = kNdBias - m;        // a weight's logarithm is zf s + zc
                 for (bool again = false;;) {             // a second time when the maximum moves
-                    // the scores' weights, their sum and the largest score; far: some row's maximum is (nib_far)
-                    auto weigh = [&](auto far_) {
-                        constexpr bool kFar = decltype(far_)::value;
-                        const bool far = kFar && nib_far(m);
-                        const float cc = far ? kNdBias : kNdBias - m, ff = far ? 1.f : fac;
-                        const float2 c0 = make_float2(cc, cc), f2 = make_float2(ff, ff);
-                        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        top = -INFINITY;
+                    const float2 c0 = make_float2(zc, zc), f2 = make_float2(zf, zf);
+                    float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    top = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float x[32];
-                            nc_ld32(s_at + 32 * c, x);
-                            mask(x, c);
-                            float tops[2] = {-INFINITY, -INFINITY};
+                    for (int c = 0; c < 2; ++c) {
+                        float x[32];
+                        nc_ld32(s_at + 32 * c, x);
+                        mask(x, c);
+                        float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int y = 0; y < 32; y += 2) {
-                                tops[(y >> 1) & 1] = fmaxf(tops[(y >> 1) & 1], fmaxf(x[y], x[y + 1]));
-                                if (far) {
-                                    x[y] = nib_far_weight(x[y], fac, m);
-                                    x[y + 1] = nib_far_weight(x[y + 1], fac, m);
-                                }
-                                const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
-                                const float2 p = make_float2(ex2(z.x), ex2(z.y));
-                                sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
-                                pk[16 * c + y / 2] = pack_half2(p.x, p.y);
-                            }
-                            top = fmaxf(top, fmaxf(tops[0], tops[1]));
+                        for (int y = 0; y < 32; y += 2) {
+                            tops[(y >> 1) & 1] = fmaxf(tops[(y >> 1) & 1], fmaxf(x[y], x[y + 1]));
+                            const float2 z = fma2(make_float2(x[y], x[y + 1]), f2, c0);
+                            const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                            sums[(y >> 1) & 1] = add2(sums[(y >> 1) & 1], p);
+                            pk[16 * c + y / 2] = pack_half2(p.x, p.y);
                         }
-                        const float2 sa = add2(sums[0], sums[1]);
-                        sum = sa.x + sa.y;
-                    };
-                    const bool any_far = __any_sync(~0u, nib_far(m));
-                    if (any_far) weigh(std::true_type{});
-                    else weigh(std::false_type{});
+                        top = fmaxf(top, fmaxf(tops[0], tops[1]));
+                    }
+                    const float2 sa = add2(sums[0], sums[1]);
+                    sum = sa.x + sa.y;
                     if (again) break;
                     // the row's maximum over both halves; two places in turn, so that one barrier a unit will do
                     float* place = ex + (units & 1u) * 4 * kNcRows;
@@ -669,11 +657,26 @@ __global__ void __launch_bounds__(kNcThreads, 1) nib_chunk_kernel(const NibGeom 
                     named_barrier(1 + t, kNcTile);
                     top = fmaxf(top, place[(hc ^ 1) * kNcRows + r]);
                     const float mx = top > -INFINITY ? top * fac : kNdNone;
-                    if (!__any_sync(~0u, mx > (any_far ? m : m + kNdLag))) break;
+                    if (!__any_sync(~0u, mx > m + kNdLag || nib_far(m))) break;
                     again = true;
                     const float mn = fmaxf(m, mx), f = ex2(m - mn);
                     m = mn;
                     l *= f;
+                    zc = kNdBias - m;
+                    if (__any_sync(~0u, nib_far(m))) {   // rounded scores in place of far rows' ones
+                        const float by = nib_far(m) ? fac : 1.f;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            float x[32];
+                            nc_ld32(s_at + 32 * c, x);
+                            uint32_t xu[32];
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) xu[y] = __float_as_uint(x[y] * by);
+                            nc_st32(s_at + 32 * c, xu);
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        if (nib_far(m)) zf = 1.f;
+                    }
                     if (u > 0) {                         // O holds the units before: these scores came after their products
 #pragma unroll 1
                         for (int c = 0; c < D / 64; ++c) {

@@ -25,9 +25,10 @@
 //    and in the value product what the rounding left, so P is good to 22 bits.
 //  - P carries 2^7: with the maximum allowed to lag 2^8 behind, it stays below 2^15, and weights
 //    down to 2^-31 keep a bit.
-//  - Weights are 2^(s fac - m) by one fma with the rounded m = s_max fac.  From |m| = 2^21 on that rounding, the
-//    same for all of a row, could carry P out of fp16: such rows take s fac rounded as m is, with no lag, so that
-//    the largest weight is 1 again.  (Scores of a million and more: a branch that others do not enter.)
+//  - Weights are 2^(s fac + (7 - m)) by one fma, with the rounded m = s_max fac.  From |m| = 2^21 on that rounding,
+//    the same for all of a row, could carry P out of fp16: such rows' scores are multiplied and rounded as m is, which
+//    leaves the largest weight at 2^0 to 2^8, and no lag is allowed.  That stands where the maximum moves, so that
+//    the other rows' loop does not know of it.
 #pragma once
 #include "dwkv_nibble.cuh"
 
@@ -145,9 +146,8 @@ __device__ __forceinline__ float nib_query_scale(const NibGeom& G, float a, floa
     return a < INFINITY ? __uint_as_float((269u - e) << 23) : __uint_as_float(0x7fc00000u);
 }
 
-// A row's maximum is so large that its scores are rounded before it is taken from them.
+// A row's maximum is so large that its scores are rounded, as it is, before it is taken from them.
 __device__ __forceinline__ bool nib_far(float m) { return fabsf(m) >= kNdFar && m > kNdNone; }
-__device__ __forceinline__ float nib_far_weight(float s, float fac, float m) { return __fadd_rn(__fmul_rn(s, fac), -m); }
 
 // Empty units counted behind each (request, kv-head): what its end costs a CTA (merging the warps,
 // writing, the next one's queries) in units, so that ranges with an end in them carry less.
@@ -386,7 +386,9 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
         const int row0 = A.cu[w.b];
         // queries as B fragments, each row as nib_query_scale says
         uint4* qs = reinterpret_cast<uint4*>(sm + L::kQ) + lane;
-        float fac[NT][2];                                // unscaled score -> log2 units, for the lane's columns
+        float fac[NT][2];                                // unscaled score -> log2 units, for the lane's columns; 1 for far rows
+        // ... and as it was, where the warp's maxima go at the segment's end
+        float* units_of = reinterpret_cast<float*>(sm + L::kMl) + warp * L::kCols + 2 * i;
         int pos[NT][2];                                  // position of the lane's columns' rows
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -424,6 +426,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
             }
             fac[nt][0] = __shfl_sync(~0u, mult, 8 * i);
             fac[nt][1] = __shfl_sync(~0u, mult, 8 * i + 4);
+            if (g == 0) *reinterpret_cast<float2*>(units_of + nt * 8) = make_float2(fac[nt][0], fac[nt][1]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = SPLIT ? ((2 * i + c) & 3) : nt * 8 + 2 * i + c;
@@ -439,7 +442,6 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
 #pragma unroll
             for (int x = 0; x < 2 * kChunks; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
         }
-        bool far = false;                                // of any of the warp's rows
         named_barrier(1, kNdThreads);
         int t0 = w.base + w.unit * kNdUnit + kNdSub * 16 * warp;
         for (int u = 0; u < cnt; ++u, t0 += kNdUnit) {
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
 #pragma unroll
                         for (int x = 0; x < 4; ++x) jump |= s[k][nt][x] > thr[nt][x & 1];
                 if (__any_sync(~0u, jump)) {             // the maximum moves: all rows take the new one
-                    far = false;
+                    bool far = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -535,10 +537,12 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                             for (int k = 1; k < kNdSub; ++k) x = fmaxf(x, fmaxf(s[k][nt][c], s[k][nt][c + 2]));
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                            x = fmaxf(m[nt][c], fac[nt][c] * fmaxf(x, __shfl_xor_sync(~0u, x, 16)));
+                            const float unit = units_of[nt * 8 + c];
+                            x = fmaxf(m[nt][c], unit * fmaxf(x, __shfl_xor_sync(~0u, x, 16)));
                             const float f = ex2(m[nt][c] - x);
                             m[nt][c] = x;
-                            thr[nt][c] = x > kNdNone && !nib_far(x) ? (x + kNdLag) / fac[nt][c] : -INFINITY;
+                            thr[nt][c] = x > kNdNone && !nib_far(x) ? (x + kNdLag) / unit : -INFINITY;
+                            fac[nt][c] = nib_far(x) ? 1.f : unit;
                             far |= nib_far(x);
                             l[nt][c] *= f;
 #pragma unroll
@@ -547,27 +551,19 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                                 o[nt][y][c + 2] *= f;
                             }
                         }
-                    far = __any_sync(~0u, far);
-                }
-                // the weights' logarithms
-                if (!far) {
-#pragma unroll
-                    for (int k = 0; k < kNdSub; ++k)
+                    if (__any_sync(~0u, far)) {          // rounded scores in place of far rows' ones
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) s[k][nt][x] = fmaf(s[k][nt][x], fac[nt][x & 1], kNdBias - m[nt][x & 1]);
-                } else {
-                    asm volatile("" ::: "memory");
+                            for (int c = 0; c < 2; ++c) {
+                                const float by = nib_far(m[nt][c]) ? units_of[nt * 8 + c] : 1.f;
 #pragma unroll
-                    for (int k = 0; k < kNdSub; ++k)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float f = fac[nt][x & 1], mm = m[nt][x & 1];
-                                s[k][nt][x] = nib_far(mm) ? kNdBias + nib_far_weight(s[k][nt][x], f, mm) : fmaf(s[k][nt][x], f, kNdBias - mm);
+                                for (int k = 0; k < kNdSub; ++k) {
+                                    s[k][nt][c] *= by;
+                                    s[k][nt][c + 2] *= by;
+                                }
                             }
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < kNdSub; ++k) {
@@ -577,7 +573,7 @@ __global__ void __launch_bounds__(kNdThreads + 32, NdLayout<D, R>::kCtas) nib_de
                         float pr[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            pr[x] = ex2(s[k][nt][x]);
+                            pr[x] = ex2(fmaf(s[k][nt][x], fac[nt][x & 1], kNdBias - m[nt][x & 1]));
                             l[nt][x & 1] += pr[x];
                         }
 #pragma unroll

@@ -8,11 +8,11 @@ namespace dwkv {
 
 // ------------------------------------------------------------------------------ launches
 // Rows x heads a request that the decode kernels take.  24 requests of 12000 tokens, d 128, 8 kv-heads:
-// 4 and 8 rows 91 us, 16 rows 125, 32 rows 250; the chunk kernel, which does 128 rows' work for one, takes
-// 300 to 315 from 1 row to 128, and 380 for 256.  One request of 16384: 32 rows 49 us, in the chunk kernel 58.
+// 4 and 8 rows 90 us, 16 rows 127, 17 to 32 rows 247 to 257; the chunk kernel, which does 128 rows' work for
+// one, takes 297 to 308 up to 128 rows, and 353 for 256.  One request of 16384: 32 rows 52 us, in the chunk kernel 58.
 constexpr int kNdRows = 32;
-// The chunk kernel's records, two of 256 rows a CTA, are the larger ones; the launches of a call run
-// one after the other and share them.
+// The chunk kernel's records, two of 256 rows a CTA, are the larger ones (43 MB at d 128, 22 MB at 64; the
+// decode kernels' take 1.3 to 4.9 MB); the launches of a call run one after the other and share them.
 size_t nib_attend_bytes(int d) { return (size_t)2 * kNibMaxSms * 2 * kNcRows * (d + 2) * 4; }
 
 template <int D, int R, bool FP16>

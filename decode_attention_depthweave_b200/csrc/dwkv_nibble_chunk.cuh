@@ -2,9 +2,10 @@
 // above kNdRows rows (query rows x query heads of a kv-head), on the 5th-generation tensor cores.
 //
 // A (256 rows x 128 tokens) unit at d = 128 is 2048 cycles of tcgen05.mma and as many of exponentials; it
-// takes 4900, bounded by the latencies and the issue slots of the softmax and unpacking warps (half of the
-// issue slots are used).  A chunk of 2048 rows of 32 heads, 8 kv-heads, at 32768 tokens: 1.13 to 1.17 ms,
-// 910 to 945 TFLOP/s (56 to 58 % of a large library matrix product's rate).  A CTA's warps:
+// takes 4800, bounded by the latencies and the issue slots of the softmax and unpacking warps (52 % of the
+// issue slots are used; at 96 registers 132 bytes are spilled, at d = 64 84).  A chunk of 2048 rows of 32 heads,
+// 8 kv-heads, at 32768 tokens: 1.13 to 1.15 ms, 925 to 940 TFLOP/s (57 to 58 % of a large library matrix
+// product's rate).  A CTA's warps:
 //   0   MMA: S = Q K^T (from shared memory), O += P V (P from tensor memory).  The warp walks and waits
 //       together, one lane issues
 //   1   loader: bulk copies of the keys' and the values' half of each 16-token block
@@ -14,7 +15,8 @@
 //       buffers of each allow), exact, written as swizzled operand tiles: half a block a warp
 // With a thread a row (eight softmax warps) a unit took 5800 cycles: two warps a scheduler, each in its own
 // chain of latencies; warps of their own for the unpacking made it no shorter, nor did a warp for the values'
-// copies, prefetches into L2, or (for items of one tile) both tiles taking turns on its units.
+// copies or prefetches into L2.  For items of one tile, both tiles taking turns on its units were faster over
+// long contexts and slower over short ones (82 against 59 us at one request of 16384).
 //
 // Two row tiles of 128 share each unpacked K / V tile and take turns on the tensor cores: while one is in
 // its softmax, the other's products run.  (Scores in two pieces of 64 tokens, so that a tile's own products

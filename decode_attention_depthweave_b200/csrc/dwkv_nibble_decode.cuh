@@ -2,11 +2,12 @@
 // rows (query rows x query heads of a kv-head), the decode and draft-verify steps.
 //
 // o = sum_t w_t v_t over t, in one pass with a running maximum and sum.  Each byte of the cache
-// (144 a token and kv-head at d = 128) is read once, but issuing instructions bounds it: every pair
-// of codes passes a LOP3 and an HFMA2 on its way to the tensor cores, and a 16-token block takes a
-// warp some 335 instructions.  Measured (bf16, d 128, 8 kv-heads, G = 4): 300 tokens 12 us, 65536
-// tokens of one request 28 us (2.7 TB/s), 8 requests of 16384 to 32768 62 us (3.8 TB/s, 58 % of a
-// copy's rate); 160 of 4096 at d 64, fp16, 29 us.
+// (144 a token and kv-head at d = 128) is read once, but latency bounds it: 3.7 warps a scheduler, each in one
+// chain of unpacking, score products, exponentials and value products, use 56 % of the issue slots and 47 %
+// of the ALU pipe (every pair of codes passes a LOP3 and an HFMA2 on its way to the tensor cores; a 16-token
+// block takes a warp some 335 instructions).  Measured (bf16, d 128, 8 kv-heads, G = 4): 300 tokens 12 to 13 us,
+// 65536 tokens of one request 29 us (2.6 TB/s), 8 requests of 16384 to 32768 61.5 us (3.8 TB/s, 59 % of a copy's
+// rate); 160 of 4096 at d 64, fp16, 29 us.
 //
 //  - Units of 16 kWarps tokens of a (request, kv-head), in one flat order, are cut into equal
 //    contiguous ranges, one a CTA: any mix of lengths loads the SMs evenly, and no host code

@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(kTabThreads) nib_tables_kernel(const NibGeom G
 
 // ------------------------------------------------------------------------------------
 // Append and read: a warp a row of keys or of values, a lane 8 channels of a head (one 16-byte load or
-// store), two lanes a block of 16; kAhead heads' loads are issued before the first is used.  Bound by the
-// bytes of the 16-bit rows (512 of 656 a token and kv-head at d = 128).  16384 rows of 8 kv-heads, d 128:
-// append 29 us (3 TB/s), read 19 us (4.5 TB/s); 8 rows are a launch's latency, 5 and 4 us.
+// store), two lanes a block of 16; kAhead heads' loads are issued before the first is used.  16384 rows of 8
+// kv-heads, d 128: append 29 us (3 TB/s), bound by issuing the quantiser's instructions (78 % of the slots while
+// it runs; both lanes of a block make its scale); read 19 us (4.5 TB/s), by the ALU pipe (79 %) that takes the codes
+// apart.  8 rows are a launch's latency, 5 and 4 us.
 // ------------------------------------------------------------------------------------
 constexpr int kRowWarps = 8;
 constexpr int kAhead = 4;

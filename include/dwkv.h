@@ -502,7 +502,8 @@ typedef struct {
 typedef struct dwkv_nibble_ctx* dwkv_nibble_handle;
 
 /* Validates a configuration without touching the GPU; bytes of a page, a pool and the arena
- * (0 if the configuration is invalid). */
+ * (0 if the configuration is invalid).  The arena holds the workspace of the longest calls: 43 MB
+ * at head_dim 128 and 22 MB at 64, one for all layers. */
 dwkv_status dwkv_nibble_config_check(const dwkv_nibble_config* cfg);
 size_t dwkv_nibble_page_bytes(const dwkv_nibble_config* cfg);
 size_t dwkv_nibble_pool_bytes(const dwkv_nibble_config* cfg);
@@ -557,6 +558,10 @@ dwkv_status dwkv_nibble_read(dwkv_nibble_handle h, int32_t n_rows, const int32_t
  * max(0, p - window + 1) <= t <= p (from 0 without a window).
  *   o = sum_t softmax_t(softmax_scale q . k_t) v_t ; lse = log sum_t exp(softmax_scale q . k_t)
  * A row that sees nothing (p < 0) gives o = 0 and lse = -inf.
+ * Scores, maxima, sums and products are fp32; queries (bf16 ones down to 2^-32 of their row's largest
+ * channel) and cached values enter the products exactly.  The softmax weights are rounded to fp16
+ * before the value product: 11 bits, below 2^-21 of the row's largest multiples of 2^-31 of it; with
+ * dtype fp16 and at most 4 rows x (num_q_heads / num_kv_heads), 22 bits.
  *   q   : device [n_rows][num_q_heads][head_dim], q_stride elements between rows (a multiple of
  *         8), 16-byte aligned
  *   out : device [n_rows][num_q_heads][head_dim]; lse: NULL or device fp32 [n_rows][num_q_heads].

@@ -149,7 +149,8 @@ class Nibble:
     """One handle on tensors that the caller owns.  Allocates the handle's arena, nothing else
     (and outputs that are not passed in).  A call's `stream` (a torch stream or a cudaStream_t; None:
     the device's current one) is the one that the call works on: what it is given has to be ready there,
-    and the arena and outputs that are allocated here are tensors of that stream."""
+    and the arena and outputs that are allocated here are tensors of that stream.  Keep the handle until
+    its calls, and graphs captured from it, have run: nothing waits for them when it goes."""
 
     def __init__(self, cfg: dwkv_nibble_config, device="cuda", stream=None):
         if not torch.cuda.is_available():
